@@ -23,6 +23,14 @@ FMT_E2M1 = 0
 FMT_E4M3 = 1
 ACT_NONE = 0
 ACT_GELU = 1
+ACT_GELU_TANH = 2
+ACT_SILU = 3
+OUT_BF16 = -1
+DTYPE_BF16 = 0
+DTYPE_F32 = 1
+NORM_NONE = 0
+NORM_LAYER = 1
+NORM_RMS = 2
 MODE_NATIVE = 0
 MODE_QDQ = 1
 
@@ -33,6 +41,14 @@ _vp, _i64, _i32, _u32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_
 class WDesc(ctypes.Structure):
     """mxq_wdesc: one linear layer's quantized weights."""
     _fields_ = [("codes", _vp), ("sf", _vp), ("bias", _vp), ("N", _i64), ("K", _i64)]
+
+
+class NormDesc(ctypes.Structure):
+    """mxq_norm_desc: the norms around a block, their vectors, gate and residual."""
+    _fields_ = [("x", _vp), ("y", _vp), ("rows", _i64), ("K", _i64), ("x_dtype", ctypes.c_int32),
+                ("vec_dtype", ctypes.c_int32), ("norm", ctypes.c_int32), ("post_norm", ctypes.c_int32),
+                ("weight", _vp), ("bias", _vp), ("post_weight", _vp), ("post_bias", _vp), ("gate", _vp),
+                ("scale", _vp), ("shift", _vp), ("rows_per_group", _i64), ("eps", ctypes.c_float)]
 
 
 SIGNATURES = {
@@ -75,6 +91,7 @@ SIGNATURES = {
     "mxq_quantize_weight_transformed": ([_vp, _i64, _i64, _vp, _i32, _vp, _vp, _vp], _i32),
     "mxq_linear_transformed": ([_vp, _i64, _i64, _vp, _vp, _i64, _vp, _i32, _vp, _i32, _vp, _i64, _vp, _vp],
                                _i32),
+    "mxq_norm_residual": ([ctypes.POINTER(NormDesc), _vp, _i32, _vp, _vp, _vp], _i32),
     "mxq_sf_to_logical": ([_vp, _i64, _i64, _vp, _vp], _i32),
     "mxq_poll_status": ([_vp], _i32),
     "mxq_set_debug": ([_u32], _i32),

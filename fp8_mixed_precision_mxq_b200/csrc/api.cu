@@ -33,6 +33,7 @@ int ok()
 
 constexpr int64_t kMaxElems = int64_t(1) << 34;  // rows*K; keeps 32-bit group / scale indices exact
 constexpr int64_t kMaxK = int64_t(1) << 16;       // K/32 < 2^11 keeps the row division of the quantizer exact
+constexpr int64_t kMaxNormK = int64_t(1) << 15;   // a norm's row stays in the registers of one CTA
 constexpr int64_t kWsAlign = 256;
 
 int64_t round_up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
@@ -49,6 +50,12 @@ int check_ptr(const void* p, const char* name, uintptr_t align = 16)
 int check_fmt(int fmt)
 {
     if (fmt != MXQ_FMT_E2M1 && fmt != MXQ_FMT_E4M3) return fail(MXQ_ERR_INVALID_ARG, "unknown format %d", fmt);
+    return MXQ_OK;
+}
+
+int check_dtype(int dt, const char* what)
+{
+    if (dt != MXQ_DTYPE_BF16 && dt != MXQ_DTYPE_F32) return fail(MXQ_ERR_INVALID_ARG, "unknown %s %d", what, dt);
     return MXQ_OK;
 }
 
@@ -848,6 +855,50 @@ int mxq_lowrank_split(const float* U, int64_t ldu, const float* S, const float* 
     return cuda_rc(launch_lowrank_split(U, ldu, S, Vh, ldvh, w_bf16, N, K, rank, l2t_bf16, l1t_bf16, resid_bf16,
                                         static_cast<cudaStream_t>(stream)),
                    "lowrank_split launch");
+}
+
+int mxq_norm_residual(const mxq_norm_desc* d, void* z, int out_fmt, void* out, void* sf, void* stream)
+{
+    if (!d) return fail(MXQ_ERR_INVALID_ARG, "norm_residual: descriptor is NULL");
+    const bool quant = out_fmt != MXQ_OUT_BF16;
+    if (quant) RETURN_IF(check_fmt(out_fmt));
+    if (d->rows <= 0 || d->K <= 0)
+        return fail(MXQ_ERR_INVALID_ARG, "norm_residual: sizes must be positive (rows=%lld K=%lld)", (long long)d->rows,
+                    (long long)d->K);
+    if (d->K % (quant ? 32 : 8) != 0)
+        return fail(MXQ_ERR_SHAPE, "norm_residual: K=%lld is not a multiple of %d", (long long)d->K, quant ? 32 : 8);
+    if (d->K > kMaxNormK || d->rows > (int64_t(1) << 31) - 129 || d->rows * d->K > kMaxElems)
+        return fail(MXQ_ERR_SHAPE, "norm_residual: tensor too large (rows=%lld K=%lld)", (long long)d->rows,
+                    (long long)d->K);
+    RETURN_IF(check_dtype(d->x_dtype, "x_dtype"));
+    RETURN_IF(check_dtype(d->vec_dtype, "vec_dtype"));
+    if (d->norm != MXQ_NORM_LAYER && d->norm != MXQ_NORM_RMS)
+        return fail(MXQ_ERR_INVALID_ARG, "norm_residual: norm must be LayerNorm or RMSNorm (got %d)", d->norm);
+    if (d->post_norm != MXQ_NORM_NONE && d->post_norm != MXQ_NORM_LAYER && d->post_norm != MXQ_NORM_RMS)
+        return fail(MXQ_ERR_INVALID_ARG, "norm_residual: unknown post_norm %d", d->post_norm);
+    if (!(d->eps >= 0.0f) || !std::isfinite(d->eps))
+        return fail(MXQ_ERR_INVALID_ARG, "norm_residual: eps must be finite and not negative");
+    if (d->rows_per_group <= 0) return fail(MXQ_ERR_INVALID_ARG, "norm_residual: rows_per_group must be positive");
+    if (!d->y_bf16 && (d->gate || d->post_norm != MXQ_NORM_NONE || z))
+        return fail(MXQ_ERR_INVALID_ARG, "norm_residual: gate, post_norm and z need y");
+    if (d->post_norm == MXQ_NORM_NONE && (d->post_weight || d->post_bias))
+        return fail(MXQ_ERR_INVALID_ARG, "norm_residual: post_weight and post_bias need a post_norm");
+    if (!quant && sf) return fail(MXQ_ERR_INVALID_ARG, "norm_residual: sf goes with a quantized output");
+    RETURN_IF(check_ptr(d->x, "x"));
+    if (d->y_bf16) {
+        RETURN_IF(check_ptr(d->y_bf16, "y"));
+        RETURN_IF(check_ptr(z, "z"));
+    }
+    RETURN_IF(check_ptr(out, quant ? "codes" : "h"));
+    if (quant) RETURN_IF(check_ptr(sf, "sf"));
+    const void* vecs[] = {d->weight, d->bias, d->post_weight, d->post_bias, d->gate, d->scale, d->shift};
+    for (const void* v : vecs)
+        if (v) RETURN_IF(check_ptr(v, "a channel vector"));
+    RETURN_IF(check_device());
+    snprintf(g_path, sizeof g_path, "norm residual ->%s",
+             !quant ? "bf16" : out_fmt == MXQ_FMT_E4M3 ? "e4m3" : "e2m1");
+    return cuda_rc(launch_norm_residual(*d, z, out_fmt, out, sf, static_cast<cudaStream_t>(stream)),
+                   "norm_residual launch");
 }
 
 int mxq_sf_to_logical(const void* sf_tiled, int64_t rows, int64_t K, void* sf_rowmajor, void* stream)

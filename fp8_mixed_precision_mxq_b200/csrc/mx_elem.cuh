@@ -64,6 +64,14 @@ __device__ __forceinline__ float e8m0_inverse(uint32_t code)
     return __uint_as_float((254u - min(code, 253u)) << 23);
 }
 
+// Byte offset of the four scale bytes of row r, k-blocks 4*atom ... 4*atom + 3, in the tiled
+// layout (one aligned 32-bit word).
+__device__ __forceinline__ size_t sf_word(int64_t r, uint32_t atom, uint32_t atoms_k)
+{
+    return (static_cast<size_t>(r >> 7) * atoms_k + atom) * 512u + static_cast<uint32_t>(r & 31) * 16u +
+           static_cast<uint32_t>((r >> 5) & 3) * 4u;
+}
+
 // ---- GELU of bf16 values ---------------------------------------------------------------
 // h = bf16(GELU(x)) for a bf16 x, GELU(x) = x/2 erfc(-x / sqrt 2) (the plain erf form) rounded
 // once to bf16, nearest with ties to even: what a bf16 network's GELU gives when computed

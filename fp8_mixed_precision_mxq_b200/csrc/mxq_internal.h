@@ -45,6 +45,11 @@ cudaError_t launch_lowrank_split(const float* U, int64_t ldu, const float* S, co
                                  cudaStream_t stream);
 cudaError_t launch_sf_to_logical(const void* sf, int64_t rows, int64_t K, void* out, cudaStream_t stream);
 
+// Norms around a block with gate, residual and quantizer (norm.cu): out is h in bf16, or the
+// codes (sf the tiled scales) when out_fmt is an MX format.
+cudaError_t launch_norm_residual(const mxq_norm_desc& d, void* z, int out_fmt, void* out, void* sf,
+                                 cudaStream_t stream);
+
 struct GemmArgs {
     const void* a_codes;
     const void* a_sf;

@@ -419,6 +419,112 @@ def sqnr(refs, tests, out=None, stream=None) -> torch.Tensor:
     return out
 
 
+_NORMS = {"none": _lib.NORM_NONE, "layer": _lib.NORM_LAYER, "rms": _lib.NORM_RMS}
+_OUTS = {"bf16": _lib.OUT_BF16, **_FMTS}
+_VEC_DTYPES = {torch.bfloat16: _lib.DTYPE_BF16, torch.float32: _lib.DTYPE_F32}
+
+
+def _pick(table, key, what):
+    if key not in table:
+        raise ValueError("%s must be one of %s, got %r" % (what, ", ".join(repr(k) for k in table if isinstance(k, str)),
+                                                           key))
+    return table[key]
+
+
+def _tensor(t, name, dtype, shape, device):
+    """t, checked to be a contiguous CUDA tensor of that dtype, shape and device."""
+    if not (t.is_cuda and t.dtype == dtype and t.is_contiguous() and t.shape == shape and t.device == device):
+        raise ValueError("%s must be a contiguous %s tensor of shape %s on %s, got %s %s on %s" % (
+            name, dtype, tuple(shape), device, t.dtype, tuple(t.shape), t.device))
+    return t
+
+
+def _on_current_device(x: torch.Tensor) -> None:
+    """The library launches on the current device: its tensors have to live there."""
+    if not x.is_cuda:
+        raise ValueError("expected CUDA tensors, got one on %s" % x.device)
+    if x.get_device() != torch.cuda.current_device():
+        raise ValueError("tensors are on %s but the current device is cuda:%d" % (x.device,
+                                                                                 torch.cuda.current_device()))
+
+
+def _group_vec(t, name, dtype, rows, K, rows_per_group, device):
+    """Pointer of per-group vectors [groups, K] ([K] for one group), or 0."""
+    if t is None:
+        return 0
+    groups = -(-rows // rows_per_group)
+    ok = t.dim() == 2 and t.shape[0] >= groups or t.dim() == 1 and groups == 1
+    if not ok or t.shape[-1] != K or t.dtype != dtype or not t.is_contiguous() or t.device != device:
+        raise ValueError("%s must be a contiguous %s tensor [%d, %d] on %s, got %s %s on %s" % (
+            name, dtype, groups, K, device, t.dtype, tuple(t.shape), t.device))
+    return t.data_ptr()
+
+
+def _rows_per_group(rows_per_group, rows):
+    if rows_per_group is None:
+        return max(1, rows)
+    if rows_per_group <= 0:
+        raise ValueError("rows_per_group must be positive, got %r" % (rows_per_group,))
+    return int(rows_per_group)
+
+
+def norm_residual(x: torch.Tensor, y: torch.Tensor | None = None, norm="layer", weight=None, bias=None, gate=None,
+                  scale=None, shift=None, rows_per_group=None, post_norm="none", post_weight=None, post_bias=None,
+                  eps=1e-6, out_fmt="bf16", z=None, h=None, codes=None, sf=None, stream=None):
+    """The norms before and after a block with its gate, residual and modulation, in one pass:
+        z = x + gate * post_norm(y),   h = norm(z) * (1 + scale) + shift
+    x [rows, K] is the residual stream (bf16 or float32; z has its type), y [rows, K] bf16 the
+    block's output (None: z is x, and x is returned as z).  norm "layer" or "rms", post_norm
+    also "none".  weight, bias, post_weight, post_bias [K], gate, scale, shift [groups, K] or
+    [K] are all bf16 or all float32; row r uses group r // rows_per_group.  Returns (z, h)
+    with h bf16, or, for out_fmt "e2m1" / "e4m3", (z, codes, tiled scales): the bits that
+    quantize_act writes for that h.  z may be x; no other output may overlap an input."""
+    _on_current_device(x)
+    if x.dim() != 2 or x.dtype not in _VEC_DTYPES or not x.is_contiguous():
+        raise ValueError("x must be a contiguous bf16 or float32 tensor [rows, K]")
+    rows, K = x.shape
+    dev = x.device
+    f = _pick(_OUTS, out_fmt, "out_fmt")
+    rpg = _rows_per_group(rows_per_group, rows)
+    vdt = next((v.dtype for v in (weight, bias, post_weight, post_bias, gate, scale, shift) if v is not None),
+               torch.float32)
+    if vdt not in _VEC_DTYPES:
+        raise ValueError("the channel vectors must be bf16 or float32, got %s" % vdt)
+    w, b, pw, pb = (0 if v is None else _tensor(v, n, vdt, (K,), dev).data_ptr()
+                    for v, n in ((weight, "weight"), (bias, "bias"), (post_weight, "post_weight"),
+                                 (post_bias, "post_bias")))
+    g, sc, sh = (_group_vec(v, n, vdt, rows, K, rpg, dev)
+                 for v, n in ((gate, "gate"), (scale, "scale"), (shift, "shift")))
+    if y is not None:
+        _tensor(y, "y", torch.bfloat16, x.shape, dev)
+        z = torch.empty_like(x) if z is None else _tensor(z, "z", x.dtype, x.shape, dev)
+    elif z is not None:
+        raise ValueError("z goes with y")
+    if f == _lib.OUT_BF16:
+        out = torch.empty((rows, K), dtype=torch.bfloat16, device=dev) if h is None else _tensor(
+            h, "h", torch.bfloat16, x.shape, dev)
+    else:
+        out, sf = _codes_out(codes, sf, rows, K, f, dev)
+    d = _lib.NormDesc(x.data_ptr(), 0 if y is None else y.data_ptr(), rows, K, _VEC_DTYPES[x.dtype],
+                      _VEC_DTYPES[vdt], _pick(_NORMS, norm, "norm"), _pick(_NORMS, post_norm, "post_norm"), w, b, pw,
+                      pb, g, sc, sh, rpg, eps)
+    check(_lib.lib().mxq_norm_residual(d, _p(z), f, _p(out), _p(None if f == _lib.OUT_BF16 else sf),
+                                       _stream(stream)), "mxq_norm_residual")
+    z = x if y is None else z
+    return (z, out) if f == _lib.OUT_BF16 else (z, out, sf)
+
+
+def _codes_out(codes, sf, rows, K, f, dev):
+    """The buffers of a quantized [rows, K] output: the caller's, checked, or new ones."""
+    nc, ns = max(1, codes_bytes(rows, K, f)), max(1, sf_bytes(rows, K))
+    for t, n, name in ((codes, nc, "codes"), (sf, ns, "sf")):
+        if t is not None and not (t.dtype == torch.uint8 and t.is_contiguous() and t.numel() >= n and t.device == dev):
+            raise ValueError("%s must be a contiguous uint8 tensor of at least %d bytes on %s" % (name, n, dev))
+    codes = torch.empty(nc, dtype=torch.uint8, device=dev) if codes is None else codes
+    sf = torch.empty(ns, dtype=torch.uint8, device=dev) if sf is None else sf
+    return codes, sf
+
+
 def lowrank_workspace_bytes(M: int, N: int, K: int, fmt="e2m1", rank=64) -> int:
     return int(_lib.lib().mxq_lowrank_workspace_bytes(M, N, K, _fmt(fmt), int(rank)))
 

@@ -64,7 +64,19 @@ typedef enum {
 
 typedef enum { MXQ_FMT_E2M1 = 0, MXQ_FMT_E4M3 = 1 } mxq_fmt;      /* activation element format */
 typedef enum { MXQ_MODE_NATIVE = 0, MXQ_MODE_QDQ = 1 } mxq_mode;  /* GEMM execution mode       */
-typedef enum { MXQ_ACT_NONE = 0, MXQ_ACT_GELU = 1 } mxq_act;       /* quantizing epilogue's activation */
+typedef enum {
+    MXQ_ACT_NONE = 0,
+    MXQ_ACT_GELU = 1,      /* v Phi(v), the erf form                                        */
+    MXQ_ACT_GELU_TANH = 2, /* v / (1 + exp(-2 sqrt(2/pi) (v + 0.044715 v^3))), the tanh form */
+    MXQ_ACT_SILU = 3       /* v / (1 + exp(-v))                                             */
+} mxq_act; /* the quantizing epilogue (mxq_gemm_quant) takes the first two */
+
+/* Output of the entry points that write bf16 or an MX-quantized operand: MXQ_OUT_BF16 or an
+ * mxq_fmt. */
+enum { MXQ_OUT_BF16 = -1 };
+
+typedef enum { MXQ_DTYPE_BF16 = 0, MXQ_DTYPE_F32 = 1 } mxq_dtype;
+typedef enum { MXQ_NORM_NONE = 0, MXQ_NORM_LAYER = 1, MXQ_NORM_RMS = 2 } mxq_norm;
 
 /* Library version (major*10000 + minor*100 + patch). */
 int mxq_version(void);
@@ -389,6 +401,47 @@ int mxq_sqnr(const void* const* ref_bf16, const void* const* test_bf16, const in
 int mxq_lowrank_split(const float* U, int64_t ldu, const float* S, const float* Vh, int64_t ldvh, const void* w_bf16,
                       int64_t N, int64_t K, int64_t rank, void* l2t_bf16, void* l1t_bf16, void* resid_bf16,
                       void* stream);
+
+/* ---- around a block's linears --------------------------------------------------------
+ * What a transformer block computes between its linears, fused with them.  The blog keeps
+ * these steps in bf16 and does not describe them; they take the linears' operands and
+ * results in this library's layouts. */
+
+/* The norms before and after a block with its gate and residual.  Per row of K channels, x
+ * the residual stream and y the block's output:
+ *   u = post(y)                             post_norm of y (MXQ_NORM_NONE: u = y)
+ *   z = x + gate[g] * u                     rounded once to the stream's type x_dtype
+ *   n = norm(z)                             of the stored z
+ *   h = bf16( n * (1 + scale[g]) + shift[g] )
+ * LayerNorm(v) = (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps), RMSNorm(v) = v /
+ * sqrt(mean(v^2) + eps), times the weight plus the bias where they are given; everything
+ * between the loads and the two roundings in binary32 (a row whose mean square is beyond
+ * binary32 has no finite result).  g = row / rows_per_group selects the row's vectors in
+ * gate, scale and shift [groups, K], groups = ceil(rows / rows_per_group). */
+typedef struct {
+    const void* x;         /* [rows, K], x_dtype                                          */
+    const void* y_bf16;    /* [rows, K] bf16, or NULL: no residual step, z = x            */
+    int64_t rows, K;
+    int32_t x_dtype;       /* mxq_dtype of x and z                                        */
+    int32_t vec_dtype;     /* mxq_dtype of all the vectors below                          */
+    int32_t norm;          /* mxq_norm, MXQ_NORM_LAYER or MXQ_NORM_RMS                    */
+    int32_t post_norm;     /* mxq_norm                                                    */
+    const void* weight;    /* [K] or NULL                                                 */
+    const void* bias;      /* [K] or NULL                                                 */
+    const void* post_weight, *post_bias; /* [K] or NULL; only with a post_norm            */
+    const void* gate;      /* [groups, K] or NULL (1); only with y                        */
+    const void* scale;     /* [groups, K] or NULL (0)                                     */
+    const void* shift;     /* [groups, K] or NULL (0)                                     */
+    int64_t rows_per_group; /* > 0                                                        */
+    float eps;             /* >= 0, finite                                                */
+} mxq_norm_desc;
+
+/* z: [rows, K] in x_dtype; required with y, NULL without.  It may be x.  out_fmt
+ * MXQ_OUT_BF16: out is h [rows, K] bf16 (K % 8 == 0), sf NULL.  MXQ_FMT_E2M1 / MXQ_FMT_E4M3:
+ * out and sf are the codes and tiled scales that mxq_quantize_act writes for h, padding
+ * included (K % 32 == 0).  K <= 32768; all pointers 16-byte aligned; except for z = x, no
+ * output may overlap an input. */
+int mxq_norm_residual(const mxq_norm_desc* d, void* z, int out_fmt, void* out, void* sf, void* stream);
 
 /* Tiled scale factors -> logical row-major [rows, K/32] bytes (for tests). */
 int mxq_sf_to_logical(const void* sf_tiled, int64_t rows, int64_t K, void* sf_rowmajor, void* stream);
