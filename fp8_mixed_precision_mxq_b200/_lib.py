@@ -51,6 +51,12 @@ class NormDesc(ctypes.Structure):
                 ("scale", _vp), ("shift", _vp), ("rows_per_group", _i64), ("eps", ctypes.c_float)]
 
 
+class Epilogue(ctypes.Structure):
+    """mxq_epilogue: activation, gate and residual of a linear's output."""
+    _fields_ = [("act", ctypes.c_int32), ("gate_dtype", ctypes.c_int32), ("residual", _vp), ("gate", _vp),
+                ("rows_per_group", _i64)]
+
+
 SIGNATURES = {
     "mxq_version": ([], _i32),
     "mxq_codes_bytes": ([_i64, _i64, _i32], _i64),
@@ -92,6 +98,16 @@ SIGNATURES = {
     "mxq_linear_transformed": ([_vp, _i64, _i64, _vp, _vp, _i64, _vp, _i32, _vp, _i32, _vp, _i64, _vp, _vp],
                                _i32),
     "mxq_norm_residual": ([ctypes.POINTER(NormDesc), _vp, _i32, _vp, _vp, _vp], _i32),
+    "mxq_gemm_residual": ([_vp, _vp, _i32, _i64, _i64, _vp, _vp, _i64, _vp, ctypes.POINTER(Epilogue), _vp, _vp],
+                          _i32),
+    "mxq_gemm_bf16_residual": ([_vp, _i64, _i64, _vp, _i64, _vp, ctypes.POINTER(Epilogue), _vp, _vp], _i32),
+    "mxq_linear_residual": ([_vp, _i64, _i64, _vp, _vp, _i64, _vp, _i32, ctypes.POINTER(Epilogue), _vp, _i64, _vp,
+                             _vp], _i32),
+    "mxq_gemm_gated": ([_vp, _vp, _i32, _i64, _i64, ctypes.POINTER(WDesc), ctypes.POINTER(WDesc), _i32, _i32, _vp,
+                        _vp, _vp], _i32),
+    "mxq_gemm_bf16_gated": ([_vp, _i64, _i64, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _vp, _vp, _vp], _i32),
+    "mxq_gated_ffn": ([_vp, _i64, _i64, ctypes.POINTER(WDesc), ctypes.POINTER(WDesc), ctypes.POINTER(WDesc), _i32,
+                       _i32, _i32, ctypes.POINTER(Epilogue), _vp, _i64, _vp, _vp], _i32),
     "mxq_sf_to_logical": ([_vp, _i64, _i64, _vp, _vp], _i32),
     "mxq_poll_status": ([_vp], _i32),
     "mxq_set_debug": ([_u32], _i32),

@@ -249,6 +249,99 @@ int64_t ffn_ws(int64_t M, int64_t K, int64_t H, int up_fmt, int down_fmt)
            round_up(codes_bytes(M, H, down_fmt), kWsAlign) + round_up(sf_bytes(M, H), kWsAlign);
 }
 
+int check_act(int act)
+{
+    if (act < MXQ_ACT_NONE || act > MXQ_ACT_SILU) return fail(MXQ_ERR_INVALID_ARG, "unknown activation %d", act);
+    return MXQ_OK;
+}
+
+int check_epilogue(const mxq_epilogue* e)
+{
+    if (!e) return fail(MXQ_ERR_INVALID_ARG, "epilogue is NULL");
+    RETURN_IF(check_act(e->act));
+    if (e->residual) RETURN_IF(check_ptr(e->residual, "residual"));
+    if (e->gate) {
+        RETURN_IF(check_dtype(e->gate_dtype, "gate_dtype"));
+        RETURN_IF(check_ptr(e->gate, "gate"));
+        if (e->rows_per_group <= 0) return fail(MXQ_ERR_INVALID_ARG, "rows_per_group must be positive");
+    }
+    return MXQ_OK;
+}
+
+void set_epilogue(GemmArgs& g, const mxq_epilogue& e)
+{
+    g.epilogue = kEpilogueResidual;
+    g.act = e.act;
+    g.residual = e.residual;
+    g.gate = e.gate;
+    g.gate_f32 = e.gate_dtype == MXQ_DTYPE_F32;
+    g.rows_per_group = e.gate ? e.rows_per_group : 1;
+}
+
+// A residual or gated GEMM: the few-row kernel, or the pair kernel.
+int run_epilogue_gemm(const GemmArgs& g, const char* what, cudaStream_t stream)
+{
+    const char* msg = nullptr;
+    int rc = g.M <= kRowsMaxM ? launch_gemm_rows(g, stream, &msg, g_path, sizeof g_path)
+                              : launch_gemm(g, stream, &msg, g_path, sizeof g_path);
+    if (rc != MXQ_OK) return fail(rc, "%s: %s", what, msg ? msg : "launch failed");
+    return ok();
+}
+
+int run_gemm_residual(const void* a_codes, const void* a_sf, int a_fmt, int64_t M, int64_t K, const void* w_codes,
+                      const void* w_sf, int64_t N, const void* bias, const mxq_epilogue& e, void* y,
+                      cudaStream_t stream)
+{
+    GemmArgs g{a_codes, a_sf, a_fmt, M, N, K, w_codes, w_sf, bias, y};
+    set_epilogue(g, e);
+    return run_epilogue_gemm(g, "gemm with residual", stream);
+}
+
+// The output of a gated GEMM: h [M, H] in bf16, or its MX form (H is the next layer's K).
+int check_gated_out(int64_t M, int64_t H, int act, int out_fmt, const void* out, const void* out_sf)
+{
+    RETURN_IF(check_act(act));
+    if (out_fmt == MXQ_OUT_BF16) {
+        if (out_sf) return fail(MXQ_ERR_INVALID_ARG, "out_sf goes with a quantized output");
+        return check_ptr(out, "out");
+    }
+    return check_gelu_quant(M, H, out_fmt, out, out_sf, nullptr);
+}
+
+int check_wdesc_pair(const mxq_wdesc* gate, const mxq_wdesc* up)
+{
+    if (!gate || !up) return fail(MXQ_ERR_INVALID_ARG, "a weight descriptor is NULL");
+    if (gate->N != up->N || gate->K != up->K)
+        return fail(MXQ_ERR_SHAPE, "the two projections differ: gate [%lld, %lld], up [%lld, %lld]", (long long)gate->N,
+                    (long long)gate->K, (long long)up->N, (long long)up->K);
+    return MXQ_OK;
+}
+
+void set_gated(GemmArgs& g, const void* w2, const void* w2_sf, const void* bias2, int act, int out_fmt, void* out,
+               void* out_sf)
+{
+    g.epilogue = kEpilogueGated;
+    g.act = act;
+    g.w2_codes = w2;
+    g.w2_sf = w2_sf;
+    g.bias2 = bias2;
+    g.out_fmt = out_fmt;
+    if (out_fmt == MXQ_OUT_BF16) {
+        g.y = out;
+    } else {
+        g.q_codes = out;
+        g.q_sf = out_sf;
+    }
+}
+
+int run_gemm_gated(const void* a_codes, const void* a_sf, int a_fmt, int64_t M, int64_t K, const mxq_wdesc& gate,
+                   const mxq_wdesc& up, int act, int out_fmt, void* out, void* out_sf, cudaStream_t stream)
+{
+    GemmArgs g{a_codes, a_sf, a_fmt, M, gate.N, K, gate.codes, gate.sf, gate.bias, nullptr};
+    set_gated(g, up.codes, up.sf, up.bias, act, out_fmt, out, out_sf);
+    return run_epilogue_gemm(g, "gated gemm", stream);
+}
+
 }  // namespace
 
 extern "C" {
@@ -901,6 +994,119 @@ int mxq_norm_residual(const mxq_norm_desc* d, void* z, int out_fmt, void* out, v
                    "norm_residual launch");
 }
 
+int mxq_gemm_residual(const void* a_codes, const void* a_sf, int a_fmt, int64_t M, int64_t K, const void* w_codes,
+                      const void* w_sf, int64_t N, const void* bias_bf16, const mxq_epilogue* e, void* y_bf16,
+                      void* stream)
+{
+    RETURN_IF(check_gemm(a_codes, a_sf, a_fmt, M, K, w_codes, w_sf, N, bias_bf16, y_bf16));
+    RETURN_IF(check_epilogue(e));
+    RETURN_IF(check_device());
+    return run_gemm_residual(a_codes, a_sf, a_fmt, M, K, w_codes, w_sf, N, bias_bf16, *e, y_bf16,
+                             static_cast<cudaStream_t>(stream));
+}
+
+int mxq_gemm_bf16_residual(const void* a_bf16, int64_t M, int64_t K, const void* b_bf16, int64_t N,
+                           const void* bias_bf16, const mxq_epilogue* e, void* y_bf16, void* stream)
+{
+    RETURN_IF(check_gemm_bf16(a_bf16, M, K, b_bf16, N, bias_bf16, y_bf16));
+    RETURN_IF(check_epilogue(e));
+    RETURN_IF(check_device());
+    GemmArgs g{a_bf16, nullptr, MXQ_FMT_E2M1, M, N, K, b_bf16, nullptr, bias_bf16, y_bf16};
+    g.bf16 = true;
+    set_epilogue(g, *e);
+    return run_epilogue_gemm(g, "bf16 gemm with residual", static_cast<cudaStream_t>(stream));
+}
+
+int mxq_linear_residual(const void* x_bf16, int64_t M, int64_t K, const void* w_codes, const void* w_sf, int64_t N,
+                        const void* bias_bf16, int act_fmt, const mxq_epilogue* e, void* workspace, int64_t ws_bytes,
+                        void* y_bf16, void* stream)
+{
+    RETURN_IF(check_ptr(x_bf16, "x"));
+    RETURN_IF(check_ptr(workspace, "workspace", kWsAlign));
+    // the workspace stands in for the quantized activation in the GEMM checks
+    RETURN_IF(check_gemm(workspace, workspace, act_fmt, M, K, w_codes, w_sf, N, bias_bf16, y_bf16));
+    RETURN_IF(check_epilogue(e));
+    const int64_t need = linear_ws(M, N, K, act_fmt, MXQ_MODE_NATIVE);
+    if (ws_bytes < need)
+        return fail(MXQ_ERR_WORKSPACE, "workspace has %lld bytes, needs %lld", (long long)ws_bytes, (long long)need);
+    RETURN_IF(check_device());
+    uint8_t* xc = static_cast<uint8_t*>(workspace);
+    uint8_t* xs = xc + round_up(codes_bytes(M, K, act_fmt), kWsAlign);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    RETURN_IF(cuda_rc(launch_quantize(x_bf16, M, K, act_fmt, xc, xs, st), "quantize launch"));
+    return run_gemm_residual(xc, xs, act_fmt, M, K, w_codes, w_sf, N, bias_bf16, *e, y_bf16, st);
+}
+
+int mxq_gemm_gated(const void* a_codes, const void* a_sf, int a_fmt, int64_t M, int64_t K, const mxq_wdesc* gate,
+                   const mxq_wdesc* up, int act, int out_fmt, void* out, void* out_sf, void* stream)
+{
+    RETURN_IF(check_wdesc_pair(gate, up));
+    if (gate->K != K)
+        return fail(MXQ_ERR_SHAPE, "gated gemm: the weights have K=%lld, the activation %lld", (long long)gate->K,
+                    (long long)K);
+    RETURN_IF(check_gated_out(M, gate->N, act, out_fmt, out, out_sf));
+    RETURN_IF(check_gemm(a_codes, a_sf, a_fmt, M, K, gate->codes, gate->sf, gate->N, gate->bias, out));
+    RETURN_IF(check_gemm(a_codes, a_sf, a_fmt, M, K, up->codes, up->sf, up->N, up->bias, out));
+    RETURN_IF(check_device());
+    return run_gemm_gated(a_codes, a_sf, a_fmt, M, K, *gate, *up, act, out_fmt, out, out_sf,
+                          static_cast<cudaStream_t>(stream));
+}
+
+int mxq_gemm_bf16_gated(const void* a_bf16, int64_t M, int64_t K, const void* gate_bf16, const void* gate_bias,
+                        const void* up_bf16, const void* up_bias, int64_t H, int act, int out_fmt, void* out,
+                        void* out_sf, void* stream)
+{
+    RETURN_IF(check_gated_out(M, H, act, out_fmt, out, out_sf));
+    RETURN_IF(check_gemm_bf16(a_bf16, M, K, gate_bf16, H, gate_bias, out));
+    RETURN_IF(check_gemm_bf16(a_bf16, M, K, up_bf16, H, up_bias, out));
+    RETURN_IF(check_device());
+    GemmArgs g{a_bf16, nullptr, MXQ_FMT_E2M1, M, H, K, gate_bf16, nullptr, gate_bias, nullptr};
+    g.bf16 = true;
+    set_gated(g, up_bf16, nullptr, up_bias, act, out_fmt, out, out_sf);
+    return run_epilogue_gemm(g, "bf16 gated gemm", static_cast<cudaStream_t>(stream));
+}
+
+int mxq_gated_ffn(const void* x_bf16, int64_t M, int64_t K, const mxq_wdesc* gate, const mxq_wdesc* up,
+                  const mxq_wdesc* down, int act, int up_fmt, int down_fmt, const mxq_epilogue* e, void* workspace,
+                  int64_t ws_bytes, void* y_bf16, void* stream)
+{
+    RETURN_IF(check_wdesc_pair(gate, up));
+    if (!down) return fail(MXQ_ERR_INVALID_ARG, "a weight descriptor is NULL");
+    const int64_t H = gate->N;
+    if (gate->K != K || down->K != H)
+        return fail(MXQ_ERR_SHAPE, "gated ffn: weights of K=%lld and K=%lld do not fit x of %lld and H=%lld",
+                    (long long)gate->K, (long long)down->K, (long long)K, (long long)H);
+    RETURN_IF(check_ptr(x_bf16, "x"));
+    RETURN_IF(check_ptr(workspace, "workspace", kWsAlign));
+    // the workspace stands in for the quantized activations in the GEMM checks
+    RETURN_IF(check_fmt(down_fmt));
+    RETURN_IF(check_gated_out(M, H, act, down_fmt, workspace, workspace));
+    RETURN_IF(check_gemm(workspace, workspace, up_fmt, M, K, gate->codes, gate->sf, H, gate->bias, workspace));
+    RETURN_IF(check_gemm(workspace, workspace, up_fmt, M, K, up->codes, up->sf, H, up->bias, workspace));
+    RETURN_IF(check_gemm(workspace, workspace, down_fmt, M, H, down->codes, down->sf, down->N, down->bias, y_bf16));
+    RETURN_IF(check_epilogue(e));
+    if (e->act != MXQ_ACT_NONE)
+        return fail(MXQ_ERR_INVALID_ARG, "gated ffn: the output's epilogue takes no activation (got %d)", e->act);
+    const int64_t need = ffn_ws(M, K, H, up_fmt, down_fmt);
+    if (ws_bytes < need)
+        return fail(MXQ_ERR_WORKSPACE, "workspace has %lld bytes, needs %lld", (long long)ws_bytes, (long long)need);
+    RETURN_IF(check_device());
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    uint8_t* xc = static_cast<uint8_t*>(workspace);
+    uint8_t* xs = xc + round_up(codes_bytes(M, K, up_fmt), kWsAlign);
+    uint8_t* hc = xs + round_up(sf_bytes(M, K), kWsAlign);
+    uint8_t* hs = hc + round_up(codes_bytes(M, H, down_fmt), kWsAlign);
+    RETURN_IF(cuda_rc(launch_quantize(x_bf16, M, K, up_fmt, xc, xs, st), "quantize launch"));
+    RETURN_IF(run_gemm_gated(xc, xs, up_fmt, M, K, *gate, *up, act, down_fmt, hc, hs, st));
+    char gp[sizeof g_path];
+    snprintf(gp, sizeof gp, "%s", g_path);
+    RETURN_IF(run_gemm_residual(hc, hs, down_fmt, M, H, down->codes, down->sf, down->N, down->bias, *e, y_bf16, st));
+    char dp[sizeof g_path];
+    snprintf(dp, sizeof dp, "%s", g_path);
+    snprintf(g_path, sizeof g_path, "gated ffn: %.110s | %.110s", gp, dp);
+    return ok();
+}
+
 int mxq_sf_to_logical(const void* sf_tiled, int64_t rows, int64_t K, void* sf_rowmajor, void* stream)
 {
     RETURN_IF(check_rows_k(rows, K, "sf_to_logical"));
@@ -913,11 +1119,13 @@ int mxq_sf_to_logical(const void* sf_tiled, int64_t rows, int64_t K, void* sf_ro
 
 int mxq_poll_status(void* stream)
 {
-    uint32_t v = 0, q = 0;
+    uint32_t v = 0, r = 0, q = 0;
     int rc = read_and_clear_device_status(static_cast<cudaStream_t>(stream), &v);
+    if (rc == MXQ_OK) rc = read_and_clear_rows_status(static_cast<cudaStream_t>(stream), &r);
     if (rc == MXQ_OK) rc = read_and_clear_quant_status(static_cast<cudaStream_t>(stream), &q);
     if (rc != MXQ_OK) return fail(rc, "reading the device status word failed");
     if (v != 0) return fail(static_cast<int>(v), "a GEMM kernel's bounded wait ran out");
+    if (r != 0) return fail(static_cast<int>(r), "a few-row GEMM kernel's bounded wait ran out");
     if (q != 0) return fail(static_cast<int>(q), "a quantizer kernel's bounded wait ran out");
     return ok();
 }

@@ -65,7 +65,7 @@ namespace {
 constexpr int BN = 256;                   // output columns per tile (both variants): 256 or 192
 // Warp roles: 0 TMA producer, 1 MMA issuer, then the epilogue warps, then one scale-copy
 // warp.  The bf16 epilogue has four warps, one per TMEM lane quarter; the quantizing
-// epilogue eight, two per lane quarter taking alternate chunks, so that its GELU
+// and residual epilogues eight, two per lane quarter taking alternate chunks, so that their
 // arithmetic has twice the warps to hide latency with.
 template <int kOut>
 constexpr int kEpiWarpsOf = kOut ? 8 : 4;
@@ -121,10 +121,25 @@ constexpr int kOutGeluE4M3 = 2;
 // path is compiled out (1-2 % faster than the variants with h, paired A/B at 720p).
 constexpr int kOutQE2M1 = 3;
 constexpr int kOutQE4M3 = 4;
+// y = bf16(residual + gate * act(acc + bias)): the linear with the rest of its block's step.
+constexpr int kOutRes = 5;
+// The gated feed-forward's two projections in one tile: columns [0, 128) of the accumulator
+// are 128 columns of x . Wg^T and [128, 256) the same columns of x . Wu^T (each CTA of the
+// pair loads one weight's 128 rows), and the epilogue writes h = bf16(act(g + bg) * (u + bu))
+// as bf16 or MX-quantized.
+constexpr int kOutGated = 6;
+constexpr int kOutGatedE2M1 = 7;
+constexpr int kOutGatedE4M3 = 8;
 template <int kOut>
-constexpr bool kOutE4M3 = kOut == kOutGeluE4M3 || kOut == kOutQE4M3;
+constexpr bool kOutE4M3 = kOut == kOutGeluE4M3 || kOut == kOutQE4M3 || kOut == kOutGatedE4M3;
+template <int kOut>  // bf16 staging buffers (y, or h on request)
+constexpr bool kOutEbuf = kOut <= kOutGeluE4M3 || kOut == kOutRes || kOut == kOutGated;
+template <int kOut>  // the next layer's MX operand is written
+constexpr bool kOutQuant = (kOut >= kOutGeluE2M1 && kOut <= kOutQE4M3) || kOut >= kOutGatedE2M1;
+template <int kOut>  // GELU from the table
+constexpr bool kOutLut = kOut >= kOutGeluE2M1 && kOut <= kOutQE4M3;
 template <int kOut>
-constexpr bool kOutEbuf = kOut <= kOutGeluE4M3;  // bf16 staging buffers (y, or h on request)
+constexpr bool kOutIsGated = kOut >= kOutGated;
 
 // Shared-memory plan of one CTA.  kPair = 1: the CTA owns a 128 x 256 tile and loads
 // all 256 weight rows; kPair = 2: a CTA pair owns a 256 x 256 tile, each CTA loads its
@@ -135,7 +150,7 @@ template <int kPair, int kOut, bool kQA = false>
 struct Cfg {
     // the quantizing epilogue's code staging takes one pipeline stage's worth of memory,
     // unless the launch writes no h (no bf16 staging then)
-    static constexpr int kStages = kQA ? 6 : kPair == 2 ? ((kOut && kOutEbuf<kOut>) ? 5 : 6) : (kOut ? 3 : 4);
+    static constexpr int kStages = kQA ? 6 : kPair == 2 ? (kOutLut<kOut> && kOutEbuf<kOut> ? 5 : 6) : (kOut ? 3 : 4);
     static constexpr int BM = 128 * kPair;
     static constexpr int kRowsB = kQA ? 128 : BN / kPair;
     static constexpr uint32_t kStageA = 128 * 128;
@@ -152,9 +167,14 @@ struct Cfg {
     // otherwise leave no room for the GELU table
     static constexpr int kQBufs = kOutE4M3<kOut> ? 1 : 2;
     static constexpr int kEpiWarps = kEpiWarpsOf<kOut>;
-    static constexpr uint32_t kOffQ = kOffEpi + (kOutEbuf<kOut> ? kEpiWarps * 2 * kEpiBuf : 0u);
-    static constexpr uint32_t kOffLut = kOffQ + (kOut ? kEpiWarps * kQBufs * kQBuf : 0u);  // GELU table
-    static constexpr uint32_t kOffBar = kOffLut + (kOut ? kGeluTableBytes : 0u);
+    // bf16 staging buffers per warp: two, or one for the eight-warp epilogues that write
+    // nothing else (a chunk's store has long been read when the warp's next chunk is ready),
+    // which keeps the sixth pipeline stage
+    static constexpr int kEbufs = kOut >= kOutRes ? 1 : 2;
+    static constexpr bool kOneBuf = kOutE4M3<kOut> || (kEbufs == 1 && kOutEbuf<kOut>);  // staging not doubled
+    static constexpr uint32_t kOffQ = kOffEpi + (kOutEbuf<kOut> ? kEpiWarps * kEbufs * kEpiBuf : 0u);
+    static constexpr uint32_t kOffLut = kOffQ + (kOutQuant<kOut> ? kEpiWarps * kQBufs * kQBuf : 0u);  // GELU table
+    static constexpr uint32_t kOffBar = kOffLut + (kOutLut<kOut> ? kGeluTableBytes : 0u);
     static constexpr uint32_t kNumBars = 2 * kStages + 6 + 2 * kSfBufs;
     static constexpr uint32_t kSmemBytes = kOffBar + kNumBars * 8 + 16;
     static constexpr int kGroupM = 32;  // tile rows (tiles along M) per rasterization group
@@ -184,7 +204,41 @@ struct Params {
     uint8_t* qa_sf;
     uint32_t qa_atoms_k;
     int qa_fmt;
+    // residual and gated epilogues: activation, and of the former the residual [M, N] and the
+    // gate's rows [groups, N] (either may be null; row m uses gate row m / rows_per_group), of
+    // the latter the second projection's bias
+    int act;
+    int gate_f32;
+    const __nv_bfloat16* res;
+    const void* gate;
+    uint32_t rows_per_group;
+    const __nv_bfloat16* bias2;
 };
+
+
+// Eight gate values (fp32 or bf16) from element i on.
+__device__ __forceinline__ void load_gate8(const void* gate, int f32, size_t i, float (&v)[8])
+{
+    if (f32) {
+        const float4* g = reinterpret_cast<const float4*>(static_cast<const float*>(gate) + i);
+        const float4 a = __ldg(g), b = __ldg(g + 1);
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    } else {
+        const uint4 a = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(gate) + i));
+        v[0] = lo_f(a.x); v[1] = hi_f(a.x); v[2] = lo_f(a.y); v[3] = hi_f(a.y);
+        v[4] = lo_f(a.z); v[5] = hi_f(a.z); v[6] = lo_f(a.w); v[7] = hi_f(a.w);
+    }
+}
+
+// Eight bias values, packed, from the lane that holds them.
+__device__ __forceinline__ void shfl_bias8(const uint4& bias8, int src, uint32_t (&b)[4])
+{
+    b[0] = __shfl_sync(0xFFFFFFFFu, bias8.x, src);
+    b[1] = __shfl_sync(0xFFFFFFFFu, bias8.y, src);
+    b[2] = __shfl_sync(0xFFFFFFFFu, bias8.z, src);
+    b[3] = __shfl_sync(0xFFFFFFFFu, bias8.w, src);
+}
 
 __device__ __forceinline__ void record_status(uint32_t code) { atomicCAS(&g_device_status, 0u, code); }
 
@@ -247,9 +301,9 @@ __global__ void __launch_bounds__(kThreadsFor<kOut, kQA>, 1)
         prefetch_tmap(&map_b);
         prefetch_tmap(&map_sfa);
         prefetch_tmap(&map_sfb);
-        if (kOut == kOutBf16 || (kOutEbuf<kOut> && p.write_h)) prefetch_tmap(&map_y);
-        if (kOut != kOutBf16) prefetch_tmap(&map_q);
-        if (p.lr_stages > 0) {
+        if (kOut == kOutBf16 || kOut >= kOutRes || (kOutEbuf<kOut> && p.write_h)) prefetch_tmap(&map_y);
+        if (kOutQuant<kOut>) prefetch_tmap(&map_q);
+        if (p.lr_stages > 0 || kOutIsGated<kOut>) {
             prefetch_tmap(&map_u);
             prefetch_tmap(&map_l2);
         }
@@ -310,20 +364,33 @@ __global__ void __launch_bounds__(kThreadsFor<kOut, kQA>, 1)
                         if (leader) mbar_arrive_expect_tx(&full[s], kTxLr);
                         tma_load_2d<kPair>(smem + C::kOffA + s * C::kStageA, &map_u, ks * 64,
                                            mb * C::BM + static_cast<int>(rank) * 128, bar, pol_a);
-                        tma_load_2d<kPair>(smem + C::kOffB + s * C::kStageB, &map_l2, ks * 64,
-                                           nb * BN + static_cast<int>(rank) * C::kRowsB, bar, pol_w);
+                        if constexpr (kOutIsGated<kOut>)  // the leader's half: Wg; the other CTA's: Wu
+                            tma_load_2d<kPair>(smem + C::kOffB + s * C::kStageB, leader ? &map_l2 : &map_b, ks * 64,
+                                               nb * C::kRowsB, bar, pol_w);
+                        else
+                            tma_load_2d<kPair>(smem + C::kOffB + s * C::kStageB, &map_l2, ks * 64,
+                                               nb * BN + static_cast<int>(rank) * C::kRowsB, bar, pol_w);
                         continue;
                     }
                     const int kq = ks - p.lr_stages;
                     if (leader) mbar_arrive_expect_tx(&full[s], kTx);
                     tma_load_2d<kPair>(smem + C::kOffA + s * C::kStageA, &map_a, kq * 128,
                                        mb * C::BM + static_cast<int>(rank) * 128, bar, pol_a);
-                    tma_load_2d<kPair>(smem + C::kOffB + s * C::kStageB, &map_b, kq * 128,
-                                       nb * BN + static_cast<int>(rank) * C::kRowsB, bar, pol_w);
                     tma_load_2d<kPair>(smem + C::kOffSFA + s * C::kStageSFA, &map_sfa, kq * AK * 128,
                                        mb * kPair + static_cast<int>(rank), bar, pol_a);
-                    tma_load_2d<kPair>(smem + C::kOffSFB + s * C::kStageSFB, &map_sfb, kq * AK * 128,
-                                       (nb * BN) / 128, bar, pol_w);
+                    if constexpr (kOutIsGated<kOut>) {
+                        // the tile's two weights, one CTA each; both CTAs need both weights' scales
+                        tma_load_2d<kPair>(smem + C::kOffB + s * C::kStageB, leader ? &map_b : &map_l2, kq * 128,
+                                           nb * C::kRowsB, bar, pol_w);
+                        tma_load_2d<kPair>(smem + C::kOffSFB + s * C::kStageSFB, &map_sfb, kq * AK * 128, nb, bar, pol_w);
+                        tma_load_2d<kPair>(smem + C::kOffSFB + s * C::kStageSFB + AK * 512, &map_u, kq * AK * 128, nb,
+                                           bar, pol_w);
+                    } else {
+                        tma_load_2d<kPair>(smem + C::kOffB + s * C::kStageB, &map_b, kq * 128,
+                                           nb * BN + static_cast<int>(rank) * C::kRowsB, bar, pol_w);
+                        tma_load_2d<kPair>(smem + C::kOffSFB + s * C::kStageSFB, &map_sfb, kq * AK * 128,
+                                           (nb * BN) / 128, bar, pol_w);
+                    }
                 }
             }
             // drain: the last stages' loads have landed once their consumer released them
@@ -574,10 +641,10 @@ __global__ void __launch_bounds__(kThreadsFor<kOut, kQA>, 1)
         const int ew = warp - 2;
         const int q = warp & 3;  // TMEM lane quarter this warp may access
         const uint32_t lanes = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
-        uint8_t* ebuf0 = smem + C::kOffEpi + ew * 2 * kEpiBuf;
+        uint8_t* ebuf0 = smem + C::kOffEpi + ew * C::kEbufs * kEpiBuf;
         uint8_t* qbuf0 = smem + C::kOffQ + ew * C::kQBufs * C::kQBuf;
         const uint16_t* lut = reinterpret_cast<const uint16_t*>(smem + C::kOffLut);
-        if constexpr (kOut != kOutBf16) {
+        if constexpr (kOutLut<kOut>) {
             // the GELU table, built by the epilogue warps while the first tile's MMAs run
             if (p.gelu)
                 gelu_table_fill(reinterpret_cast<uint16_t*>(smem + C::kOffLut), threadIdx.x - 64u, kEpiWarps * 32u);
@@ -595,7 +662,42 @@ __global__ void __launch_bounds__(kThreadsFor<kOut, kQA>, 1)
             // the load latency hides behind the tile's MMAs; chunks fetch them by shuffle
             uint4 bias8 = make_uint4(0u, 0u, 0u, 0u);
             const int nbias = nb * BN + 8 * lane;
-            if (has_bias && nbias + 8 <= p.N) bias8 = __ldg(reinterpret_cast<const uint4*>(p.bias + nbias));
+            if constexpr (kOutIsGated<kOut>) {
+                // lanes 0-15: the gate projection's bias of tile columns 8*lane ..; lanes 16-31: the other's
+                const __nv_bfloat16* b = lane < 16 ? p.bias : p.bias2;
+                const int nh = nb * C::kRowsB + 8 * (lane & 15);
+                if (b != nullptr && nh + 8 <= p.N) bias8 = __ldg(reinterpret_cast<const uint4*>(b + nh));
+            } else {
+                if (has_bias && nbias + 8 <= p.N) bias8 = __ldg(reinterpret_cast<const uint4*>(p.bias + nbias));
+            }
+            // residual epilogue: this lane's output row, the gate's values of tile columns
+            // 8*lane .. for the first row's group (the whole warp's, nearly always), and the
+            // residual of the warp's first chunk, all on their way before the wait
+            [[maybe_unused]] int res_row = 0;
+            [[maybe_unused]] bool gate_shared = true;
+            [[maybe_unused]] float gate8[8];
+            [[maybe_unused]] uint4 res4[4];
+            [[maybe_unused]] auto load_res = [&](int c) __attribute__((always_inline)) {
+                const int n = nb * BN + c * 32;
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    res4[g] = make_uint4(0u, 0u, 0u, 0u);
+                    if (p.res != nullptr && res_row < p.M && n + 8 * g < p.N)
+                        res4[g] = __ldcs(reinterpret_cast<const uint4*>(p.res + static_cast<size_t>(res_row) * p.N + n) + g);
+                }
+            };
+            if constexpr (kOut == kOutRes) {
+                const int first = mb * C::BM + static_cast<int>(rank) * 128 + q * 32;
+                res_row = first + lane;
+                if (p.gate != nullptr) {
+                    const uint32_t g0 = static_cast<uint32_t>(min(first, p.M - 1)) / p.rows_per_group;
+                    gate_shared = g0 == static_cast<uint32_t>(min(first + 31, p.M - 1)) / p.rows_per_group;
+                    const bool in = nbias + 8 <= p.N;
+                    load_gate8(p.gate, p.gate_f32, static_cast<size_t>(g0) * p.N + (in ? nbias : 0), gate8);
+                }
+                const int grp = ew >> 2;
+                load_res(slot ? grp : BN / 32 - kOvl + grp);
+            }
             const bool waited = mbar_wait(&tmem_full[slot], (tcount >> 1) & 1, kWaitNs);
             if (!__all_sync(0xFFFFFFFFu, waited)) {  // the warp leaves together (tcgen05.ld is .aligned)
                 if (lane == 0) record_status(MXQ_ERR_TIMEOUT);
@@ -619,10 +721,136 @@ __global__ void __launch_bounds__(kThreadsFor<kOut, kQA>, 1)
                     if (lane == 0) mbar_arrive_cluster(ci == last ? tmem_empty_bar : bar_overlap);
                 }
             };
-            // a ring of kLdBufs chunk registers: the first kLdBufs loads go out back to back, so
-            // the shared columns (kOverlapChunks <= kLdBufs chunks) are released after one wait
+            // writes 32 columns of the tile (from output column n) whose bf16 values are o, staged
+            // and by TMA: as they are, or as the next layer's MX block of each row; returns the
+            // block's scale byte
+            auto emit = [&](const uint32_t(&o)[16], int n) __attribute__((always_inline)) -> uint32_t {
+                uint32_t sc_byte = 0u;
+                                    const bool store_y = kOut == kOutBf16 || kOut >= kOutRes || (kOutEbuf<kOut> && p.write_h);
+                                    uint8_t* buf = ebuf0 + (C::kEbufs == 2 ? eb : 0) * kEpiBuf;
+                                    // the stores that last used this chunk's buffers have read them
+                                    if (lane == 0) {
+                                        if constexpr (C::kOneBuf)
+                                            bulk_wait_read<0>();
+                                        else
+                                            bulk_wait_read<1>();
+                                    }
+                                    __syncwarp();
+                                    if (kOutEbuf<kOut> && store_y) {
+                                        const uint32_t rsw = (static_cast<uint32_t>(lane) >> 1) & 3u;
+                #pragma unroll
+                                        for (int ch = 0; ch < 4; ++ch) {
+                                            uint4* dst = reinterpret_cast<uint4*>(buf + lane * 64 + ((ch ^ rsw) * 16));
+                                            *dst = make_uint4(o[4 * ch], o[4 * ch + 1], o[4 * ch + 2], o[4 * ch + 3]);
+                                        }
+                                    }
+                                    if constexpr (kOutQuant<kOut>) {
+                                        // this lane's 32 values are one MX block of the next layer's K: its
+                                        // E8M0 scale and element codes, rounded to nearest even by cvt
+                                        constexpr uint32_t kEmax = kOutE4M3<kOut> ? 8u : 2u;
+                                        uint32_t m2 = o[0];
+                #pragma unroll
+                                        for (int i = 1; i < 16; ++i) m2 = absmax_bf16x2(m2, o[i]);
+                                        m2 = absmax_bf16x2(m2, __byte_perm(m2, 0, 0x1032));
+                                        const uint32_t sc = e8m0_code<kEmax>(m2);
+                                        const float inv = e8m0_inverse(sc);
+                                        const uint32_t keep = sc == 255u ? 0u : 0xFFFFFFFFu;  // a non-finite block: codes 0
+                                        uint8_t* qb = qbuf0 + (C::kQBufs == 2 ? eb : 0) * C::kQBuf;
+                                        if constexpr (!kOutE4M3<kOut>) {
+                                            uint32_t cw[4];
+                                            const float2 inv2 = make_float2(inv, inv);
+                #pragma unroll
+                                            for (int k = 0; k < 4; ++k) {
+                                                float v[8];
+                #pragma unroll
+                                                for (int i = 0; i < 4; ++i) {
+                                                    const float2 f = __fmul2_rn(make_float2(lo_f(o[4 * k + i]), hi_f(o[4 * k + i])), inv2);
+                                                    v[2 * i] = f.x;
+                                                    v[2 * i + 1] = f.y;
+                                                }
+                                                cw[k] = cvt_e2m1x8(v) & keep;
+                                            }
+                                            *reinterpret_cast<uint4*>(qb + lane * 16) = make_uint4(cw[0], cw[1], cw[2], cw[3]);
+                                        } else {
+                                            uint32_t cw[8];
+                                            const float2 inv2 = make_float2(inv, inv);
+                #pragma unroll
+                                            for (int k = 0; k < 8; ++k) {
+                                                const float2 f0 = __fmul2_rn(make_float2(lo_f(o[2 * k]), hi_f(o[2 * k])), inv2);
+                                                const float2 f1 = __fmul2_rn(make_float2(lo_f(o[2 * k + 1]), hi_f(o[2 * k + 1])), inv2);
+                                                cw[k] = (cvt_e4m3x2(f0.x, f0.y) | (cvt_e4m3x2(f1.x, f1.y) << 16)) & keep;
+                                            }
+                                            *reinterpret_cast<uint4*>(qb + lane * 32) = make_uint4(cw[0], cw[1], cw[2], cw[3]);
+                                            *reinterpret_cast<uint4*>(qb + lane * 32 + 16) = make_uint4(cw[4], cw[5], cw[6], cw[7]);
+                                        }
+                                        sc_byte = sc;
+                                    }
+                                    fence_async_smem();
+                                    __syncwarp();
+                                    if (lane == 0) {
+                                        if (kOutEbuf<kOut> && store_y) tma_store_2d(&map_y, buf, n, row0, pol_y);
+                                        if constexpr (kOutQuant<kOut>)
+                                            tma_store_2d(&map_q, qbuf0 + (C::kQBufs == 2 ? eb : 0) * C::kQBuf,
+                                                         kOutE4M3<kOut> ? n : n / 2, row0,
+                                                         pol_y);
+                                        bulk_commit();
+                                    }
+                eb ^= 1;
+                return sc_byte;
+            };
+            [[maybe_unused]] auto store_scale = [&](int c, uint32_t sc_byte) __attribute__((always_inline)) {
+                // this row's scale byte of k-block nb*8 + c, straight into the tiled
+                // layout; rows between M and the 128-row padding, and k-blocks past N
+                // inside the padding, get 0 as the layout requires
+                const int row = row0 + lane;
+                const uint32_t kb = static_cast<uint32_t>(nb) * (kOutIsGated<kOut> ? 4u : 8u) + static_cast<uint32_t>(c);
+                if (row < p.q_rows_pad && kb < 4u * p.q_atoms_k) {
+                    const size_t off = (static_cast<size_t>(row >> 7) * p.q_atoms_k + (kb >> 2)) * 512u +
+                                       (row & 31) * 16u + ((row >> 5) & 3) * 4u + (kb & 3u);
+                    p.q_sf[off] = row < p.M ? static_cast<uint8_t>(sc_byte) : uint8_t(0);
+                }
+            };
             // one 32-column chunk (the ci-th in drain order) whose accumulators are in acc
-            auto process = [&](const uint32_t(&acc)[32], int ci) __attribute__((always_inline)) {
+            [[maybe_unused]] auto process_res = [&](const uint32_t(&acc)[32], int ci, int ci_next)
+                __attribute__((always_inline)) {
+                const int c = chunk_of(ci);
+                const int n = nb * BN + c * 32;
+                uint4 res[4];
+#pragma unroll
+                for (int g = 0; g < 4; ++g) res[g] = res4[g];
+                if (ci_next >= 0) load_res(chunk_of(ci_next));  // lands during this chunk's work
+                if (n >= p.N) return;  // warp-uniform
+                uint32_t o[16];
+                with_act(p.act, [&](auto act) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {  // 8 columns at a time
+                        uint32_t b[4];
+                        shfl_bias8(bias8, 4 * c + k, b);
+                        const uint32_t r[4] = {res[k].x, res[k].y, res[k].z, res[k].w};
+                        float gt[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) gt[i] = 1.0f;
+                        if (p.gate != nullptr) {
+                            if (gate_shared) {
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) gt[i] = __shfl_sync(0xFFFFFFFFu, gate8[i], 4 * c + k);
+                            } else if (n + 8 * k < p.N) {  // the warp's rows span two groups
+                                const uint32_t gr = static_cast<uint32_t>(min(res_row, p.M - 1)) / p.rows_per_group;
+                                load_gate8(p.gate, p.gate_f32, static_cast<size_t>(gr) * p.N + n + 8 * k, gt);
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int e = 8 * k + 2 * i;
+                            const float v0 = act_f32<act>(__uint_as_float(acc[e]) + lo_f(b[i]));
+                            const float v1 = act_f32<act>(__uint_as_float(acc[e + 1]) + hi_f(b[i]));
+                            o[4 * k + i] = bf16x2_bits(fmaf(v0, gt[2 * i], lo_f(r[i])), fmaf(v1, gt[2 * i + 1], hi_f(r[i])));
+                        }
+                    }
+                });
+                emit(o, n);
+            };
+            [[maybe_unused]] auto process = [&](const uint32_t(&acc)[32], int ci) __attribute__((always_inline)) {
                 const int c = chunk_of(ci);
                 uint32_t sc_byte = 0u;  // quantizing epilogue: the chunk's E8M0 scale
                 const int n = nb * BN + c * 32;
@@ -665,91 +893,65 @@ __global__ void __launch_bounds__(kThreadsFor<kOut, kQA>, 1)
                         chunk_out(std::true_type{});
                     else
                         chunk_out(std::false_type{});
-                    const bool store_y = kOut == kOutBf16 || (kOutEbuf<kOut> && p.write_h);
-                    uint8_t* buf = ebuf0 + eb * kEpiBuf;
-                    // the stores that last used this chunk's buffers have read them
-                    if (lane == 0) {
-                        if constexpr (C::kQBufs == 1)
-                            bulk_wait_read<0>();
-                        else
-                            bulk_wait_read<1>();
-                    }
-                    __syncwarp();
-                    if (store_y) {
-                        const uint32_t rsw = (static_cast<uint32_t>(lane) >> 1) & 3u;
+                    sc_byte = emit(o, n);
+                }
+                if constexpr (kOutQuant<kOut>) store_scale(c, sc_byte);
+            };
+            if constexpr (kOutIsGated<kOut>) {
+                // Two warps per lane quarter take two of the four 32-column chunks of h each.  A
+                // chunk needs both halves of the accumulator, so a warp's four loads go out
+                // together and the accumulator slot is handed back at once, before the
+                // arithmetic.
+                static_assert(!kOutIsGated<kOut> || (kPair == 2 && BN == 256 && kChunks == 8), "gated tile");
+                const int c0 = (ew >> 2) * 2;
+                uint32_t ga[2][32], ua[2][32];
 #pragma unroll
-                        for (int ch = 0; ch < 4; ++ch) {
-                            uint4* dst = reinterpret_cast<uint4*>(buf + lane * 64 + ((ch ^ rsw) * 16));
-                            *dst = make_uint4(o[4 * ch], o[4 * ch + 1], o[4 * ch + 2], o[4 * ch + 3]);
-                        }
-                    }
-                    if constexpr (kOut != kOutBf16) {
-                        // this lane's 32 values are one MX block of the next layer's K: its
-                        // E8M0 scale and element codes, rounded to nearest even by cvt
-                        constexpr uint32_t kEmax = kOutE4M3<kOut> ? 8u : 2u;
-                        uint32_t m2 = o[0];
+                for (int j = 0; j < 2; ++j) {
+                    tmem_ld_x32(lanes + col0 + (c0 + j) * 32, ga[j]);
+                    tmem_ld_x32(lanes + col0 + C::kRowsB + (c0 + j) * 32, ua[j]);
+                }
+                tmem_ld_wait();
 #pragma unroll
-                        for (int i = 1; i < 16; ++i) m2 = absmax_bf16x2(m2, o[i]);
-                        m2 = absmax_bf16x2(m2, __byte_perm(m2, 0, 0x1032));
-                        const uint32_t sc = e8m0_code<kEmax>(m2);
-                        const float inv = e8m0_inverse(sc);
-                        const uint32_t keep = sc == 255u ? 0u : 0xFFFFFFFFu;  // a non-finite block: codes 0
-                        uint8_t* qb = qbuf0 + (C::kQBufs == 2 ? eb : 0) * C::kQBuf;
-                        if constexpr (!kOutE4M3<kOut>) {
-                            uint32_t cw[4];
-                            const float2 inv2 = make_float2(inv, inv);
+                for (int j = 0; j < 2; ++j) {
+                    tmem_regs_ready(ga[j]);
+                    tmem_regs_ready(ua[j]);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive_cluster(bar_overlap);
+                    mbar_arrive_cluster(tmem_empty_bar);
+                }
+                auto gated_chunk = [&](const uint32_t(&g)[32], const uint32_t(&u)[32], int c)
+                    __attribute__((always_inline)) {
+                    const int n = nb * C::kRowsB + c * 32;
+                    uint32_t sc_byte = 0u;
+                    if (n < p.N) {  // warp-uniform
+                        uint32_t o[16];
+                        with_act(p.act, [&](auto act) {
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
-                                float v[8];
+                                uint32_t bg[4], bu[4];  // 8 columns of the two biases, packed
+                                shfl_bias8(bias8, 4 * c + k, bg);
+                                shfl_bias8(bias8, 16 + 4 * c + k, bu);
 #pragma unroll
                                 for (int i = 0; i < 4; ++i) {
-                                    const float2 f = __fmul2_rn(make_float2(lo_f(o[4 * k + i]), hi_f(o[4 * k + i])), inv2);
-                                    v[2 * i] = f.x;
-                                    v[2 * i + 1] = f.y;
+                                    const int e = 8 * k + 2 * i;
+                                    const float g0 = __uint_as_float(g[e]) + lo_f(bg[i]);
+                                    const float g1 = __uint_as_float(g[e + 1]) + hi_f(bg[i]);
+                                    const float u0 = __uint_as_float(u[e]) + lo_f(bu[i]);
+                                    const float u1 = __uint_as_float(u[e + 1]) + hi_f(bu[i]);
+                                    o[4 * k + i] = bf16x2_bits(act_f32<act>(g0) * u0, act_f32<act>(g1) * u1);
                                 }
-                                cw[k] = cvt_e2m1x8(v) & keep;
                             }
-                            *reinterpret_cast<uint4*>(qb + lane * 16) = make_uint4(cw[0], cw[1], cw[2], cw[3]);
-                        } else {
-                            uint32_t cw[8];
-                            const float2 inv2 = make_float2(inv, inv);
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                const float2 f0 = __fmul2_rn(make_float2(lo_f(o[2 * k]), hi_f(o[2 * k])), inv2);
-                                const float2 f1 = __fmul2_rn(make_float2(lo_f(o[2 * k + 1]), hi_f(o[2 * k + 1])), inv2);
-                                cw[k] = (cvt_e4m3x2(f0.x, f0.y) | (cvt_e4m3x2(f1.x, f1.y) << 16)) & keep;
-                            }
-                            *reinterpret_cast<uint4*>(qb + lane * 32) = make_uint4(cw[0], cw[1], cw[2], cw[3]);
-                            *reinterpret_cast<uint4*>(qb + lane * 32 + 16) = make_uint4(cw[4], cw[5], cw[6], cw[7]);
-                        }
-                        sc_byte = sc;
+                        });
+                        sc_byte = emit(o, n);
                     }
-                    fence_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (store_y) tma_store_2d(&map_y, buf, n, row0, pol_y);
-                        if constexpr (kOut != kOutBf16)
-                            tma_store_2d(&map_q, qbuf0 + (C::kQBufs == 2 ? eb : 0) * C::kQBuf,
-                                         kOutE4M3<kOut> ? n : n / 2, row0,
-                                         pol_y);
-                        bulk_commit();
-                    }
-                    eb ^= 1;
-                }
-                if constexpr (kOut != kOutBf16) {
-                    // this row's scale byte of k-block nb*8 + c, straight into the tiled
-                    // layout; rows between M and the 128-row padding, and k-blocks past N
-                    // inside the padding, get 0 as the layout requires
-                    const int row = row0 + lane;
-                    const uint32_t kb = static_cast<uint32_t>(nb) * 8u + static_cast<uint32_t>(c);
-                    if (row < p.q_rows_pad && kb < 4u * p.q_atoms_k) {
-                        const size_t off = (static_cast<size_t>(row >> 7) * p.q_atoms_k + (kb >> 2)) * 512u +
-                                           (row & 31) * 16u + ((row >> 5) & 3) * 4u + (kb & 3u);
-                        p.q_sf[off] = row < p.M ? static_cast<uint8_t>(sc_byte) : uint8_t(0);
-                    }
-                }
-            };
-            if constexpr (kOut == kOutBf16) {
+                    if constexpr (kOutQuant<kOut>) store_scale(c, sc_byte);
+                };
+                gated_chunk(ga[0], ua[0], c0);
+                gated_chunk(ga[1], ua[1], c0 + 1);
+            } else if constexpr (kOut == kOutBf16) {
                 // a ring of kLdBufs chunk registers, fully unrolled: the first kLdBufs loads go
                 // out back to back, so the shared columns are released after one wait
                 uint32_t r[kLdb][32];
@@ -794,7 +996,10 @@ __global__ void __launch_bounds__(kThreadsFor<kOut, kQA>, 1)
                 landed(1, last_shared, kMine - 1);
 #pragma unroll 1
                 for (int i = 0; i < kMine; ++i) {
-                    process(ra, grp + 2 * i);
+                    if constexpr (kOut == kOutRes)
+                        process_res(ra, grp + 2 * i, i + 1 < kMine ? grp + 2 * (i + 1) : -1);
+                    else
+                        process(ra, grp + 2 * i);
                     if (i + 1 < kMine) {
                         if (i >= 1) {  // chunk i+1, loaded during this chunk's work
                             tmem_ld_wait();
@@ -904,10 +1109,26 @@ cudaError_t launch_out(int out, const CUtensorMap& ma, const CUtensorMap& mb, co
         return launch_variant<kW4A8, kPair, kOutQE2M1>(ma, mb, msa, msb, my, mq, mu, ml, p, grid, stream);
     if (out == kOutQE4M3)
         return launch_variant<kW4A8, kPair, kOutQE4M3>(ma, mb, msa, msb, my, mq, mu, ml, p, grid, stream);
+    if constexpr (kPair == 2) {
+        if (out == kOutRes)
+            return launch_variant<kW4A8, kPair, kOutRes>(ma, mb, msa, msb, my, mq, mu, ml, p, grid, stream);
+        if (out == kOutGated)
+            return launch_variant<kW4A8, kPair, kOutGated>(ma, mb, msa, msb, my, mq, mu, ml, p, grid, stream);
+        if (out == kOutGatedE2M1)
+            return launch_variant<kW4A8, kPair, kOutGatedE2M1>(ma, mb, msa, msb, my, mq, mu, ml, p, grid, stream);
+        if (out == kOutGatedE4M3)
+            return launch_variant<kW4A8, kPair, kOutGatedE4M3>(ma, mb, msa, msb, my, mq, mu, ml, p, grid, stream);
+    }
     return launch_variant<kW4A8, kPair, kOutBf16>(ma, mb, msa, msb, my, mq, mu, ml, p, grid, stream);
 }
 
 }  // namespace
+
+const char* epilogue_name(const GemmArgs& g)
+{
+    if (g.epilogue == kEpilogueResidual) return " +act+residual";
+    return g.out_fmt < 0 ? " +gated->bf16" : g.out_fmt == kFmtE4M3 ? " +gated->e4m3" : " +gated->e2m1";
+}
 
 int launch_gemm(const GemmArgs& g, cudaStream_t stream, const char** msg, char* path, size_t path_len)
 {
@@ -915,6 +1136,8 @@ int launch_gemm(const GemmArgs& g, cudaStream_t stream, const char** msg, char* 
     const bool w4a8 = !bf16 && g.a_fmt == kFmtE4M3;
     const bool quant_out = g.out_fmt >= 0;
     const bool quant_a = bf16 && g.qa_fmt >= 0;
+    const bool gated = g.epilogue == kEpilogueGated;
+    const bool residual = g.epilogue == kEpilogueResidual;
     if (quant_a && (g.N > 128 || quant_out || g.qa_codes == nullptr || g.qa_sf == nullptr)) {
         *msg = "quantizing A beside a bf16 GEMM needs N <= 128, a bf16 output and both MX buffers";
         return MXQ_ERR_INVALID_ARG;
@@ -922,7 +1145,9 @@ int launch_gemm(const GemmArgs& g, cudaStream_t stream, const char** msg, char* 
     // CTA pairs for anything taller than one 128-row tile; a lone CTA otherwise, and for the
     // bf16 GEMM that quantizes its A (each CTA's quantizer waits on its own stage barriers,
     // where a pair's loads all complete on the leader's).
-    const int pair = g.M > 128 && !quant_a ? 2 : 1;
+    // The residual and gated epilogues always run on pairs (few rows have a kernel of their
+    // own, gemm_rows.cu).
+    const int pair = gated || residual || (g.M > 128 && !quant_a) ? 2 : 1;
     const int rows_b = BN / pair;
     const int64_t atoms_k = sf_atoms_k(g.K);
     const int ak = w4a8 ? 1 : 2;
@@ -942,7 +1167,14 @@ int launch_gemm(const GemmArgs& g, cudaStream_t stream, const char** msg, char* 
         ok = ok && make_map_2d(&msa, CU_TENSOR_MAP_DATA_TYPE_UINT32, g.a_sf, atoms_k * 128, ceil_div(g.M, 128),
                                atoms_k * 512, ak * 128, 1, CU_TENSOR_MAP_SWIZZLE_NONE);
         ok = ok && make_map_2d(&msb, CU_TENSOR_MAP_DATA_TYPE_UINT32, g.w_sf, atoms_k * 128, ceil_div(g.N, 128),
-                               atoms_k * 512, ak * 128, 2, CU_TENSOR_MAP_SWIZZLE_NONE);
+                               atoms_k * 512, ak * 128, gated ? 1 : 2, CU_TENSOR_MAP_SWIZZLE_NONE);
+        if (gated) {  // the second weight takes the maps of the low-rank branch, which it excludes
+            ok = ok && make_map_2d(&ml, w4a8 ? CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B : CU_TENSOR_MAP_DATA_TYPE_UINT8,
+                                   g.w2_codes, w4a8 ? g.K : g.K / 2, g.N, g.K / 2, 128, rows_b,
+                                   CU_TENSOR_MAP_SWIZZLE_128B);
+            ok = ok && make_map_2d(&mu, CU_TENSOR_MAP_DATA_TYPE_UINT32, g.w2_sf, atoms_k * 128, ceil_div(g.N, 128),
+                                   atoms_k * 512, ak * 128, 1, CU_TENSOR_MAP_SWIZZLE_NONE);
+        }
     }
     // bf16 output (y, or h of the quantizing epilogue): 32 x 32 boxes, 64-byte swizzle
     const void* ybase = g.y ? g.y : g.q_codes;  // without h the map is never used
@@ -972,7 +1204,10 @@ int launch_gemm(const GemmArgs& g, cudaStream_t stream, const char** msg, char* 
     if (bf16) {
         ma = msa = mu;  // never used without block-scaled stages
         mb = msb = ml;
-    } else if (lr_stages == 0) {
+        if (gated)
+            ok = ok && make_map_2d(&mb, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, g.w2_codes, lr_k, g.N, lr_k * 2, 64, rows_b,
+                                   CU_TENSOR_MAP_SWIZZLE_128B);
+    } else if (lr_stages == 0 && !gated) {
         mu = ma;  // never used without bf16 stages
         ml = mb;
     }
@@ -986,14 +1221,14 @@ int launch_gemm(const GemmArgs& g, cudaStream_t stream, const char** msg, char* 
     p.N = static_cast<int>(g.N);
     p.K = static_cast<int>(g.K);
     p.m_blocks = static_cast<int>(ceil_div(g.M, 128 * pair));
-    p.n_blocks = static_cast<int>(ceil_div(g.N, BN));
+    p.n_blocks = static_cast<int>(ceil_div(g.N, gated ? rows_b : BN));
     p.num_tiles = p.m_blocks * p.n_blocks;
     p.k_stages = bf16 ? 0 : static_cast<int>(ceil_div(g.K, w4a8 ? 128 : 256));
     p.debug = g_debug_flags;
     p.q_sf = static_cast<uint8_t*>(g.q_sf);
     p.q_atoms_k = quant_out ? static_cast<uint32_t>(sf_atoms_k(g.N)) : 0u;
     p.q_rows_pad = static_cast<int>(ceil_div(g.M, 128) * 128);
-    p.write_h = quant_out && g.y != nullptr ? 1 : 0;
+    p.write_h = quant_out && !gated && g.y != nullptr ? 1 : 0;
     p.gelu = g.out_gelu ? 1 : 0;
     p.alpha = g.alpha;
     p.lr_stages = lr_stages;
@@ -1005,7 +1240,15 @@ int launch_gemm(const GemmArgs& g, cudaStream_t stream, const char** msg, char* 
     p.qa_sf = static_cast<uint8_t*>(g.qa_sf);
     p.qa_atoms_k = quant_a ? static_cast<uint32_t>(sf_atoms_k(g.K)) : 0u;
     p.qa_fmt = quant_a ? g.qa_fmt : -1;
-    const int out = !quant_out  ? kOutBf16
+    p.act = g.act;
+    p.res = static_cast<const __nv_bfloat16*>(g.residual);
+    p.gate = g.gate;
+    p.gate_f32 = g.gate_f32 ? 1 : 0;
+    p.rows_per_group = static_cast<uint32_t>(std::min<int64_t>(g.rows_per_group, g.M));
+    p.bias2 = static_cast<const __nv_bfloat16*>(g.bias2);
+    const int out = gated       ? (!quant_out ? kOutGated : g.out_fmt == kFmtE4M3 ? kOutGatedE4M3 : kOutGatedE2M1)
+                    : residual  ? kOutRes
+                    : !quant_out ? kOutBf16
                     : p.write_h ? (g.out_fmt == kFmtE4M3 ? kOutGeluE4M3 : kOutGeluE2M1)
                                 : (g.out_fmt == kFmtE4M3 ? kOutQE4M3 : kOutQE2M1);
 
@@ -1030,11 +1273,11 @@ int launch_gemm(const GemmArgs& g, cudaStream_t stream, const char** msg, char* 
     if (path && bf16)
         snprintf(path, path_len, "bf16 kind::f16 %s %dx%d (mma n %d) grid %d tiles %d%s", pair == 2 ? "2cta" : "1cta",
                  128 * pair, BN, p.mma_n, grid, p.num_tiles,
-                 quant_a ? (g.qa_fmt == kFmtE4M3 ? " +quantize a->e4m3" : " +quantize a->e2m1") : "");
+                 gated || residual ? epilogue_name(g) : quant_a ? (g.qa_fmt == kFmtE4M3 ? " +quantize a->e4m3" : " +quantize a->e2m1") : "");
     else if (path)
         snprintf(path, path_len, "native %s %s %dx%d grid %d tiles %d%s%s", w4a8 ? "mxf8f6f4" : "mxf4",
                  pair == 2 ? "2cta" : "1cta", 128 * pair, BN, grid, p.num_tiles,
-                 !quant_out ? "" : g.out_gelu ? (g.out_fmt == kFmtE4M3 ? " +gelu->e4m3" : " +gelu->e2m1")
+                 gated || residual ? epilogue_name(g) : !quant_out ? "" : g.out_gelu ? (g.out_fmt == kFmtE4M3 ? " +gelu->e4m3" : " +gelu->e2m1")
                                               : (g.out_fmt == kFmtE4M3 ? " +quant->e4m3" : " +quant->e2m1"),
                  lr_stages ? " +lowrank(bf16 f16-mma)" : "");
     return MXQ_OK;

@@ -8,6 +8,10 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include <type_traits>
+
+#include "mxq.h"
+
 namespace mxq {
 
 // Packed max of |a| and |b| over two bf16 lanes (sign of the result is the xor of the
@@ -120,6 +124,41 @@ __device__ __forceinline__ uint32_t gelu_bf16_bits(uint32_t b, const uint16_t* l
     uint32_t big = neg ? 0x8000u : b;
     if (m >= 0x7F80u) big = (m == 0x7F80u && !neg) ? b : 0x7FC0u;
     return in ? t : (m < kGeluLo ? half : big);
+}
+
+// ---- activations in binary32 ------------------------------------------------------------
+// Applied to the binary32 sum, so that the result is rounded to bf16 once.  The two sigmoid
+// forms v / (1 + exp(-t)) keep their relative accuracy where v is far negative (1 + tanh would
+// cancel there), and the erf form uses erfc for the same reason.
+template <int kAct>
+__device__ __forceinline__ float act_f32(float v)
+{
+    if constexpr (kAct == MXQ_ACT_SILU) {
+        return __fdividef(v, 1.0f + __expf(-v));
+    } else if constexpr (kAct == MXQ_ACT_GELU_TANH) {
+        constexpr float kTwoRoot = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+        return __fdividef(v, 1.0f + __expf(-kTwoRoot * fmaf(0.044715f * v * v, v, v)));
+    } else if constexpr (kAct == MXQ_ACT_GELU) {
+        return 0.5f * v * erfcf(v * -0.70710678118654752f);
+    }
+    return v;
+}
+
+// f(integral constant of the activation): the choice is taken once, outside f's loops.
+template <class F>
+__device__ __forceinline__ void with_act(int act, F&& f)
+{
+    if (act == MXQ_ACT_SILU) f(std::integral_constant<int, MXQ_ACT_SILU>{});
+    else if (act == MXQ_ACT_GELU_TANH) f(std::integral_constant<int, MXQ_ACT_GELU_TANH>{});
+    else if (act == MXQ_ACT_GELU) f(std::integral_constant<int, MXQ_ACT_GELU>{});
+    else f(std::integral_constant<int, MXQ_ACT_NONE>{});
+}
+
+// Two fp32 values rounded to bf16, the first in the low half.
+__device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi)
+{
+    __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&h);
 }
 
 }  // namespace mxq

@@ -50,6 +50,10 @@ cudaError_t launch_sf_to_logical(const void* sf, int64_t rows, int64_t K, void* 
 cudaError_t launch_norm_residual(const mxq_norm_desc& d, void* z, int out_fmt, void* out, void* sf,
                                  cudaStream_t stream);
 
+constexpr int kEpiloguePlain = 0;
+constexpr int kEpilogueResidual = 1;
+constexpr int kEpilogueGated = 2;
+
 struct GemmArgs {
     const void* a_codes;
     const void* a_sf;
@@ -82,15 +86,36 @@ struct GemmArgs {
     int qa_fmt = -1;
     void* qa_codes = nullptr;
     void* qa_sf = nullptr;
+    // kEpilogueResidual: y = bf16(residual + gate * act(acc + bias)), residual bf16 [M, N] and
+    // gate [groups, N] (bf16, or fp32 with gate_f32; row m uses gate row m / rows_per_group) or
+    // null.  kEpilogueGated: h = bf16(act(acc + bias) * (acc2 + bias2)) with acc2 the product
+    // with the second weight; y receives h, or q_codes / q_sf its MX form (out_fmt).
+    int epilogue = kEpiloguePlain;
+    int act = MXQ_ACT_NONE;
+    const void* residual = nullptr;
+    const void* gate = nullptr;
+    bool gate_f32 = false;
+    int64_t rows_per_group = 1;
+    const void* w2_codes = nullptr;
+    const void* w2_sf = nullptr;
+    const void* bias2 = nullptr;
 };
 
 // Builds the tensor maps and launches the tcgen05 GEMM.  Returns an mxq_status;
 // on failure *msg points to a static description.
 int launch_gemm(const GemmArgs& g, cudaStream_t stream, const char** msg, char* path, size_t path_len);
 
-// Device status words written by kernels whose bounded waits ran out (the GEMM's and
+const char* epilogue_name(const GemmArgs& g);  // for the path description
+
+// The residual or gated GEMM for at most kRowsMaxM activation rows (gemm_rows.cu); arguments
+// and results as launch_gemm's.
+constexpr int64_t kRowsMaxM = 64;
+int launch_gemm_rows(const GemmArgs& g, cudaStream_t stream, const char** msg, char* path, size_t path_len);
+
+// Device status words written by kernels whose bounded waits ran out (the GEMMs' and
 // the quantizers'); each call synchronizes the stream, returns the word and clears it.
 int read_and_clear_device_status(cudaStream_t stream, uint32_t* out);
+int read_and_clear_rows_status(cudaStream_t stream, uint32_t* out);
 int read_and_clear_quant_status(cudaStream_t stream, uint32_t* out);
 
 // 2-D tiled tensor map (dims d0 inner, d1 outer; row stride in bytes; box b0 x b1);

@@ -377,15 +377,28 @@ __device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, uint32_t (&r)[32])
         : "memory");
 }
 
+// Each thread of a warp reads 16 consecutive 32-bit TMEM columns of its own lane.
+__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
-// After tmem_ld_wait(): ties the 32 destination registers of a finished tcgen05.ld to
+// After tmem_ld_wait(): ties the destination registers of a finished tcgen05.ld to
 // the wait, so the compiler cannot schedule a use of them above it (the registers of
 // an asynchronous load hold garbage until the wait).
-__device__ __forceinline__ void tmem_regs_ready(uint32_t (&r)[32])
+template <int kN>
+__device__ __forceinline__ void tmem_regs_ready(uint32_t (&r)[kN])
 {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
+    for (int i = 0; i < kN; ++i) asm volatile("" : "+r"(r[i]));
 }
 
 // Each thread of a warp writes 4 consecutive 32-bit TMEM columns of its own lane.

@@ -525,6 +525,175 @@ def _codes_out(codes, sf, rows, K, f, dev):
     return codes, sf
 
 
+_ACTS = {"none": _lib.ACT_NONE, "gelu": _lib.ACT_GELU, "gelu_tanh": _lib.ACT_GELU_TANH, "silu": _lib.ACT_SILU}
+
+
+def _act(a) -> int:
+    return _pick(_ACTS, a, "act")
+
+
+def _epilogue(act, residual, gate, rows_per_group, M, N, dev):
+    """The checked mxq_epilogue of an [M, N] output."""
+    rpg = _rows_per_group(rows_per_group, M)
+    if residual is not None:
+        _tensor(residual, "residual", torch.bfloat16, (M, N), dev)
+    gdt = torch.bfloat16 if gate is None else gate.dtype
+    if gdt not in _VEC_DTYPES:
+        raise ValueError("gate must be bf16 or float32, got %s" % gdt)
+    return _lib.Epilogue(_act(act), _VEC_DTYPES[gdt], 0 if residual is None else residual.data_ptr(),
+                         _group_vec(gate, "gate", gdt, M, N, rpg, dev), rpg)
+
+
+def _check_operand(codes, sf, M, K, f):
+    """The device of a quantized [M, K] operand, its buffers checked."""
+    _on_current_device(codes)
+    for t, n, name in ((codes, codes_bytes(M, K, f), "a_codes"), (sf, sf_bytes(M, K), "a_sf")):
+        if not t.is_contiguous() or t.numel() * t.element_size() < n or t.device != codes.device:
+            raise ValueError("%s must be a contiguous tensor of at least %d bytes on %s" % (name, n, codes.device))
+    return codes.device
+
+
+def _check_qweight(w: QWeight, name, dev):
+    if w.codes.device != dev or w.sf.device != dev or w.bias is not None and w.bias.device != dev:
+        raise ValueError("%s must be on %s" % (name, dev))
+    if w.bias is not None:
+        _tensor(w.bias, name + ".bias", torch.bfloat16, (w.N,), dev)
+
+
+def _check_x(x):
+    _on_current_device(x)
+    _cuda_bf16(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be [M, K], got %s" % (tuple(x.shape),))
+    return x.device
+
+
+def _workspace(ws, need, dev):
+    if ws is None:
+        return torch.empty(max(1, need), dtype=torch.uint8, device=dev)
+    if ws.device != dev or not ws.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on %s" % dev)
+    return ws
+
+
+def _bf16_out(out, M, N, dev):
+    return torch.empty((M, N), dtype=torch.bfloat16, device=dev) if out is None else _tensor(
+        out, "out", torch.bfloat16, (M, N), dev)
+
+
+def gemm_residual(a_codes, a_sf, fmt, M: int, K: int, w: QWeight, act="none", residual=None, gate=None,
+                  rows_per_group=None, out=None, stream=None):
+    """y = residual + gate * act(a . deq(w)^T + bias) [M, N] bf16, rounded once, on an
+    already-quantized activation.  act "none", "gelu", "gelu_tanh" or "silu"; residual [M, N]
+    bf16 (it may be out); gate [groups, N] or [N], bf16 or float32, row m using group
+    m // rows_per_group (default: one group)."""
+    f = _fmt(fmt)
+    dev = _check_operand(a_codes, a_sf, M, K, f)
+    _check_qweight(w, "w", dev)
+    e = _epilogue(act, residual, gate, rows_per_group, M, w.N, dev)
+    out = _bf16_out(out, M, w.N, dev)
+    check(_lib.lib().mxq_gemm_residual(_p(a_codes), _p(a_sf), f, M, K, _p(w.codes), _p(w.sf), w.N, _p(w.bias), e,
+                                       _p(out), _stream(stream)), "mxq_gemm_residual")
+    return out
+
+
+def gemm_bf16_residual(a: torch.Tensor, b: torch.Tensor, bias: torch.Tensor | None = None, act="none", residual=None,
+                       gate=None, rows_per_group=None, out=None, stream=None):
+    """y = residual + gate * act(a . b^T + bias) in bf16 with fp32 accumulation, a [M, K] and
+    b [N, K] bf16; the other arguments as for gemm_residual."""
+    dev = _check_x(a)
+    M, K = a.shape
+    N = b.shape[0]
+    _tensor(b, "b", torch.bfloat16, (N, K), dev)
+    if bias is not None:
+        _tensor(bias, "bias", torch.bfloat16, (N,), dev)
+    e = _epilogue(act, residual, gate, rows_per_group, M, N, dev)
+    out = _bf16_out(out, M, N, dev)
+    check(_lib.lib().mxq_gemm_bf16_residual(_p(a), M, K, _p(b), N, _p(bias), e, _p(out), _stream(stream)),
+          "mxq_gemm_bf16_residual")
+    return out
+
+
+def linear_residual(x: torch.Tensor, w: QWeight, fmt="e2m1", act="none", residual=None, gate=None,
+                    rows_per_group=None, workspace=None, out=None, stream=None):
+    """linear() with gemm_residual's epilogue: x quantized on the fly to fmt, then
+    y = residual + gate * act(x . deq(w)^T + bias)."""
+    dev = _check_x(x)
+    M, K = x.shape
+    f = _fmt(fmt)
+    _check_qweight(w, "w", dev)
+    e = _epilogue(act, residual, gate, rows_per_group, M, w.N, dev)
+    workspace = _workspace(workspace, workspace_bytes(M, w.N, K, f, MODE_NATIVE), dev)
+    out = _bf16_out(out, M, w.N, dev)
+    check(_lib.lib().mxq_linear_residual(_p(x), M, K, _p(w.codes), _p(w.sf), w.N, _p(w.bias), f, e, _p(workspace),
+                                         workspace.numel() * workspace.element_size(), _p(out), _stream(stream)),
+          "mxq_linear_residual")
+    return out
+
+
+def _gated_out(M, H, out_fmt, out, codes, sf, dev):
+    """(out_fmt, h or codes, scales) of a gated GEMM."""
+    f = _pick(_OUTS, out_fmt, "out_fmt")
+    if f == _lib.OUT_BF16:
+        return f, _bf16_out(out, M, H, dev), None
+    codes, sf = _codes_out(codes, sf, M, H, f, dev)
+    return f, codes, sf
+
+
+def gemm_gated(a_codes, a_sf, fmt, M: int, K: int, gate: QWeight, up: QWeight, act="silu", out_fmt="bf16", out=None,
+               codes=None, sf=None, stream=None):
+    """h = act(a . deq(gate)^T + gate.bias) * (a . deq(up)^T + up.bias) [M, H] in one kernel,
+    on an already-quantized activation.  Returns h in bf16, or, for out_fmt "e2m1" / "e4m3",
+    (codes, tiled scales): the bits that quantize_act writes for that h."""
+    f = _fmt(fmt)
+    dev = _check_operand(a_codes, a_sf, M, K, f)
+    _check_qweight(gate, "gate", dev)
+    _check_qweight(up, "up", dev)
+    of, o, so = _gated_out(M, gate.N, out_fmt, out, codes, sf, dev)
+    check(_lib.lib().mxq_gemm_gated(_p(a_codes), _p(a_sf), f, M, K, gate.desc(), up.desc(), _act(act), of, _p(o),
+                                    _p(so), _stream(stream)), "mxq_gemm_gated")
+    return o if so is None else (o, so)
+
+
+def gemm_bf16_gated(a: torch.Tensor, gate: torch.Tensor, up: torch.Tensor, gate_bias=None, up_bias=None, act="silu",
+                    out_fmt="bf16", out=None, codes=None, sf=None, stream=None):
+    """gemm_gated on bf16 operands: a [M, K], gate and up [H, K]."""
+    dev = _check_x(a)
+    M, K = a.shape
+    H = gate.shape[0]
+    for t, name in ((gate, "gate"), (up, "up")):
+        _tensor(t, name, torch.bfloat16, (H, K), dev)
+    for t, name in ((gate_bias, "gate_bias"), (up_bias, "up_bias")):
+        if t is not None:
+            _tensor(t, name, torch.bfloat16, (H,), dev)
+    of, o, so = _gated_out(M, H, out_fmt, out, codes, sf, dev)
+    check(_lib.lib().mxq_gemm_bf16_gated(_p(a), M, K, _p(gate), _p(gate_bias), _p(up), _p(up_bias), H, _act(act), of,
+                                         _p(o), _p(so), _stream(stream)), "mxq_gemm_bf16_gated")
+    return o if so is None else (o, so)
+
+
+def gated_ffn(x: torch.Tensor, gate: QWeight, up: QWeight, down: QWeight, act="silu", up_fmt="e2m1",
+              down_fmt="e2m1", residual=None, out_gate=None, rows_per_group=None, workspace=None, out=None,
+              stream=None):
+    """The gated feed-forward network y = residual + out_gate * (quant(act(x . gate^T) *
+    (x . up^T)) . down^T), biases included, with x quantized to up_fmt and the hidden
+    activation kept quantized in down_fmt.  residual, out_gate and rows_per_group as
+    gemm_residual's residual, gate and rows_per_group; workspace of
+    ffn_workspace_bytes(M, K, H, up_fmt, down_fmt) bytes."""
+    dev = _check_x(x)
+    M, K = x.shape
+    for w, name in ((gate, "gate"), (up, "up"), (down, "down")):
+        _check_qweight(w, name, dev)
+    e = _epilogue("none", residual, out_gate, rows_per_group, M, down.N, dev)
+    uf, df = _fmt(up_fmt), _fmt(down_fmt)
+    workspace = _workspace(workspace, ffn_workspace_bytes(M, K, gate.N, uf, df), dev)
+    out = _bf16_out(out, M, down.N, dev)
+    check(_lib.lib().mxq_gated_ffn(_p(x), M, K, gate.desc(), up.desc(), down.desc(), _act(act), uf, df, e,
+                                   _p(workspace), workspace.numel() * workspace.element_size(), _p(out),
+                                   _stream(stream)), "mxq_gated_ffn")
+    return out
+
+
 def lowrank_workspace_bytes(M: int, N: int, K: int, fmt="e2m1", rank=64) -> int:
     return int(_lib.lib().mxq_lowrank_workspace_bytes(M, N, K, _fmt(fmt), int(rank)))
 

@@ -443,6 +443,60 @@ typedef struct {
  * output may overlap an input. */
 int mxq_norm_residual(const mxq_norm_desc* d, void* z, int out_fmt, void* out, void* sf, void* stream);
 
+/* What a linear's epilogue does after its bias (mxq_gemm_residual and the entry points built
+ * on it): y = bf16( residual + gate[g] * act(sum + bias) ), everything in binary32 and rounded
+ * once.  Row m uses the gate's row g = m / rows_per_group. */
+typedef struct {
+    int32_t act;            /* mxq_act                                                    */
+    int32_t gate_dtype;     /* mxq_dtype of gate                                          */
+    const void* residual;   /* [M, N] bf16, or NULL (0); may be y                         */
+    const void* gate;       /* [groups, N], groups = ceil(M / rows_per_group), or NULL (1) */
+    int64_t rows_per_group; /* > 0                                                        */
+} mxq_epilogue;
+
+/* mxq_gemm with activation, gate and residual in its epilogue.  Arguments and limits as for
+ * mxq_gemm; residual and gate 16-byte aligned.  Up to 64 rows run on a kernel of their own that
+ * streams the weight (the tokens are the MMA's N dimension, K is split over a cluster); its
+ * sums are formed in another order than the large kernel's. */
+int mxq_gemm_residual(const void* a_codes, const void* a_sf, int a_fmt, int64_t M, int64_t K, const void* w_codes,
+                      const void* w_sf, int64_t N, const void* bias_bf16, const mxq_epilogue* e, void* y_bf16,
+                      void* stream);
+
+/* The same on bf16 operands, as mxq_gemm_bf16 takes them. */
+int mxq_gemm_bf16_residual(const void* a_bf16, int64_t M, int64_t K, const void* b_bf16, int64_t N,
+                           const void* bias_bf16, const mxq_epilogue* e, void* y_bf16, void* stream);
+
+/* mxq_linear (mode NATIVE) with that epilogue: x quantized to act_fmt into the workspace of
+ * mxq_workspace_bytes(M, N, K, act_fmt, MXQ_MODE_NATIVE) bytes, then mxq_gemm_residual. */
+int mxq_linear_residual(const void* x_bf16, int64_t M, int64_t K, const void* w_codes, const void* w_sf, int64_t N,
+                        const void* bias_bf16, int act_fmt, const mxq_epilogue* e, void* workspace, int64_t ws_bytes,
+                        void* y_bf16, void* stream);
+
+/* The two projections of a gated feed-forward network, their activation and their product in
+ * one kernel:
+ *   h = bf16( act(a . gate^T + gate.bias) * (a . up^T + up.bias) )     [M, H], H = gate.N = up.N
+ * with a the quantized activation (as for mxq_gemm; W4A8 needs K % 128 == 0 and 32-byte
+ * aligned weights).  out_fmt MXQ_OUT_BF16: out receives h (H % 8 == 0), out_sf NULL.
+ * MXQ_FMT_E2M1 / MXQ_FMT_E4M3: out and out_sf receive the codes and tiled scales that
+ * mxq_quantize_act writes for h, padding included (H % 32 == 0, H <= 65536). */
+int mxq_gemm_gated(const void* a_codes, const void* a_sf, int a_fmt, int64_t M, int64_t K, const mxq_wdesc* gate,
+                   const mxq_wdesc* up, int act, int out_fmt, void* out, void* out_sf, void* stream);
+
+/* The same on bf16 operands: a [M, K], gate and up [H, K] (K % 8 == 0), their biases [H] or
+ * NULL. */
+int mxq_gemm_bf16_gated(const void* a_bf16, int64_t M, int64_t K, const void* gate_bf16, const void* gate_bias,
+                        const void* up_bf16, const void* up_bias, int64_t H, int act, int out_fmt, void* out,
+                        void* out_sf, void* stream);
+
+/* The gated feed-forward network: x quantized to up_fmt, mxq_gemm_gated with its h quantized
+ * to down_fmt, then mxq_gemm_residual with the down weight and epilogue e (its act
+ * MXQ_ACT_NONE).  x [M, K]; gate, up: N = H, K = K; down: K = H; y [M, down.N].  down_fmt E4M3
+ * needs H % 128 == 0.  workspace: mxq_ffn_workspace_bytes(M, K, H, up_fmt, down_fmt) bytes,
+ * 256-byte aligned. */
+int mxq_gated_ffn(const void* x_bf16, int64_t M, int64_t K, const mxq_wdesc* gate, const mxq_wdesc* up,
+                  const mxq_wdesc* down, int act, int up_fmt, int down_fmt, const mxq_epilogue* e, void* workspace,
+                  int64_t ws_bytes, void* y_bf16, void* stream);
+
 /* Tiled scale factors -> logical row-major [rows, K/32] bytes (for tests). */
 int mxq_sf_to_logical(const void* sf_tiled, int64_t rows, int64_t K, void* sf_rowmajor, void* stream);
 
