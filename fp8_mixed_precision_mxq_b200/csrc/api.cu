@@ -290,9 +290,11 @@ int run_epilogue_gemm(const GemmArgs& g, const char* what, cudaStream_t stream)
 
 int run_gemm_residual(const void* a_codes, const void* a_sf, int a_fmt, int64_t M, int64_t K, const void* w_codes,
                       const void* w_sf, int64_t N, const void* bias, const mxq_epilogue& e, void* y,
-                      cudaStream_t stream)
+                      cudaStream_t stream, const void* x = nullptr, bool early = false)
 {
     GemmArgs g{a_codes, a_sf, a_fmt, M, N, K, w_codes, w_sf, bias, y};
+    g.x = x;
+    g.early = early;
     set_epilogue(g, e);
     return run_epilogue_gemm(g, "gemm with residual", stream);
 }
@@ -335,9 +337,11 @@ void set_gated(GemmArgs& g, const void* w2, const void* w2_sf, const void* bias2
 }
 
 int run_gemm_gated(const void* a_codes, const void* a_sf, int a_fmt, int64_t M, int64_t K, const mxq_wdesc& gate,
-                   const mxq_wdesc& up, int act, int out_fmt, void* out, void* out_sf, cudaStream_t stream)
+                   const mxq_wdesc& up, int act, int out_fmt, void* out, void* out_sf, cudaStream_t stream,
+                   const void* x = nullptr)
 {
     GemmArgs g{a_codes, a_sf, a_fmt, M, gate.N, K, gate.codes, gate.sf, gate.bias, nullptr};
+    g.x = x;
     set_gated(g, up.codes, up.sf, up.bias, act, out_fmt, out, out_sf);
     return run_epilogue_gemm(g, "gated gemm", stream);
 }
@@ -1021,18 +1025,23 @@ int mxq_linear_residual(const void* x_bf16, int64_t M, int64_t K, const void* w_
                         const void* bias_bf16, int act_fmt, const mxq_epilogue* e, void* workspace, int64_t ws_bytes,
                         void* y_bf16, void* stream)
 {
+    const bool fused = M <= kRowsMaxQuantM;  // x is quantized inside the GEMM kernel
     RETURN_IF(check_ptr(x_bf16, "x"));
-    RETURN_IF(check_ptr(workspace, "workspace", kWsAlign));
-    // the workspace stands in for the quantized activation in the GEMM checks
-    RETURN_IF(check_gemm(workspace, workspace, act_fmt, M, K, w_codes, w_sf, N, bias_bf16, y_bf16));
+    if (!fused) RETURN_IF(check_ptr(workspace, "workspace", kWsAlign));
+    // x stands in for the quantized activation in the GEMM checks
+    RETURN_IF(check_gemm(x_bf16, x_bf16, act_fmt, M, K, w_codes, w_sf, N, bias_bf16, y_bf16));
     RETURN_IF(check_epilogue(e));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (fused) {
+        RETURN_IF(check_device());
+        return run_gemm_residual(nullptr, nullptr, act_fmt, M, K, w_codes, w_sf, N, bias_bf16, *e, y_bf16, st, x_bf16);
+    }
     const int64_t need = linear_ws(M, N, K, act_fmt, MXQ_MODE_NATIVE);
     if (ws_bytes < need)
         return fail(MXQ_ERR_WORKSPACE, "workspace has %lld bytes, needs %lld", (long long)ws_bytes, (long long)need);
     RETURN_IF(check_device());
     uint8_t* xc = static_cast<uint8_t*>(workspace);
     uint8_t* xs = xc + round_up(codes_bytes(M, K, act_fmt), kWsAlign);
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
     RETURN_IF(cuda_rc(launch_quantize(x_bf16, M, K, act_fmt, xc, xs, st), "quantize launch"));
     return run_gemm_residual(xc, xs, act_fmt, M, K, w_codes, w_sf, N, bias_bf16, *e, y_bf16, st);
 }
@@ -1096,11 +1105,13 @@ int mxq_gated_ffn(const void* x_bf16, int64_t M, int64_t K, const mxq_wdesc* gat
     uint8_t* xs = xc + round_up(codes_bytes(M, K, up_fmt), kWsAlign);
     uint8_t* hc = xs + round_up(sf_bytes(M, K), kWsAlign);
     uint8_t* hs = hc + round_up(codes_bytes(M, H, down_fmt), kWsAlign);
-    RETURN_IF(cuda_rc(launch_quantize(x_bf16, M, K, up_fmt, xc, xs, st), "quantize launch"));
-    RETURN_IF(run_gemm_gated(xc, xs, up_fmt, M, K, *gate, *up, act, down_fmt, hc, hs, st));
+    const bool fused = M <= kRowsMaxQuantM;  // x is quantized inside the first kernel
+    if (!fused) RETURN_IF(cuda_rc(launch_quantize(x_bf16, M, K, up_fmt, xc, xs, st), "quantize launch"));
+    RETURN_IF(run_gemm_gated(xc, xs, up_fmt, M, K, *gate, *up, act, down_fmt, hc, hs, st, fused ? x_bf16 : nullptr));
     char gp[sizeof g_path];
     snprintf(gp, sizeof gp, "%s", g_path);
-    RETURN_IF(run_gemm_residual(hc, hs, down_fmt, M, H, down->codes, down->sf, down->N, down->bias, *e, y_bf16, st));
+    RETURN_IF(run_gemm_residual(hc, hs, down_fmt, M, H, down->codes, down->sf, down->N, down->bias, *e, y_bf16, st,
+                                nullptr, M <= kRowsMaxM));
     char dp[sizeof g_path];
     snprintf(dp, sizeof dp, "%s", g_path);
     snprintf(g_path, sizeof g_path, "gated ffn: %.110s | %.110s", gp, dp);

@@ -7,14 +7,21 @@
 // and add their partial sums through distributed shared memory, so that every SM streams
 // weights even when there are few tiles.  Two CTAs fit an SM.
 //   warp 0      TMA producer: weight tile(s), activation rows and their scale atoms into the
-//               shared-memory ring;
-//   warp 1      allocates TMEM; copies each stage's scales into it (tcgen05.cp) and issues the
-//               stage's MMAs (both from one thread, in order);
+//               shared-memory ring; it fills the ring before the rest of the CTA is set up;
+//   warp 1      allocates TMEM and issues each stage's MMAs;
+//   warps 2, 3  copy each stage's scales into the stage's own TMEM columns (tcgen05.cp) ahead of
+//               the MMAs, the weights' and the activation's;
+//   warps 4-7   (kQX: up to 16 rows of bf16 x) quantize each stage's part of x straight into the
+//               stage, a launch and a round trip through memory less;
 //   warps 4-7   read the accumulators (lane = weight row, column = token) into shared memory;
-// then all warps finish the cluster's tokens, rank r those with t % S == r: sums the S
-// partials in rank order (the result does not depend on timing), and applies bias, activation,
-// gate and residual, or the gated product and the MX quantization (32 lanes = 32 consecutive
-// outputs = one MX block).
+// then all warps finish the cluster's tokens in fours, rank a % S the a-th four: read the S
+// partials (one 16-byte load a rank), add them in rank order (the result does not depend on
+// timing), and apply bias, activation, gate and residual, or the gated product and the MX
+// quantization (32 lanes = 32 consecutive outputs = one MX block).
+// Launches are programmatic: the set-up runs while the kernel before on the stream ends.  All
+// global reads and writes come after griddepcontrol.wait, except that the second kernel of the
+// gated network starts on its weight before it (the first kernel allows that only after its own
+// wait, so whatever wrote the weight has long completed).
 // Every wait is bounded; one that runs out records MXQ_ERR_TIMEOUT, the copies in flight are
 // waited for, TMEM is freed and no output is written.
 #include <cuda_bf16.h>
@@ -52,21 +59,22 @@ struct Cfg {
     static constexpr uint32_t kTileX = kNT * 128;
     static constexpr uint32_t kSf = kAtoms * 512;
     static constexpr uint32_t kStage = kW * kTileW + kTileX;
+    static constexpr uint32_t kPart = kW * kNT * 128 * 4;  // a CTA's partial sums, over its stages
     // As many stages as let two CTAs share an SM's 228 KB (1 KB of each is the system's)
     static constexpr uint32_t kBudget = 115712 - 512;
     static constexpr int kStages = static_cast<int>(kBudget / (kStage + (kW + 1) * kSf));
     static constexpr uint32_t kOffX = kW * kTileW;  // inside a stage
-    static constexpr uint32_t kOffSf = kStages * kStage;
+    static constexpr uint32_t kOffSf = kStages * kStage;  // [operand][stage][kSf], the weights first
     static constexpr uint32_t kOffBar = kOffSf + kStages * (kW + 1) * kSf;
-    static constexpr uint32_t kSmem = kOffBar + (2 * kStages + 1) * 8 + 16;
-    // bytes a stage's copies report: TMA counts what it writes, except that the expanded
-    // weight counts its packed bytes
-    static constexpr uint32_t kTx = kW * (kKind == kMxf8 ? kTileW / 2 : kTileW) + kTileX + (kW + 1) * kSf;
-    // TMEM: kW accumulators of kNT columns, then 4 columns per scale atom
+    static constexpr uint32_t kSmem = kOffBar + (3 * kStages + 1) * 8 + 16;
+    // bytes a stage's tensor copies report: TMA counts what it writes, except that the
+    // expanded weight counts its packed bytes
+    static constexpr uint32_t kTxW = kW * (kKind == kMxf8 ? kTileW / 2 : kTileW);
+    // TMEM: kW accumulators of kNT columns, then each stage's scales, 4 columns an atom
     static constexpr uint32_t kSfCol = kW * kNT;
-    static constexpr uint32_t kCols = kSfCol + (kW + 1) * kAtoms * 4;
+    static constexpr uint32_t kSfCols = (kW + 1) * kAtoms * 4;
+    static constexpr uint32_t kCols = kSfCol + kStages * kSfCols;
     static constexpr uint32_t kTmem = kCols <= 32 ? 32 : kCols <= 64 ? 64 : kCols <= 128 ? 128 : 256;
-    static constexpr uint32_t kPart = kW * kNT * 128 * 4;  // fp32 partials, over the stages
     static_assert(kStages >= 2 && kCols <= 256 && kPart <= kStages * kStage, "few-row GEMM plan");
     static_assert(kStage % 1024 == 0, "swizzled tiles are 1024-byte aligned");
     static_assert(3 * (kSmem + 1024) > 233472, "at most two CTAs an SM: they may take half its TMEM each");
@@ -80,6 +88,12 @@ struct RowsParams {
     uint32_t rows_per_group;
     uint32_t atoms_n;  // scale atoms of a quantized h's row
     uint32_t debug;
+    const uint8_t* sf_w;   // tiled scales: the weight's, the second weight's, the activation's
+    const uint8_t* sf_w2;
+    const uint8_t* sf_x;
+    uint32_t atoms_k;      // scale atoms of a row of K
+    int early;         // the weight may be read before the kernel before on the stream has ended
+    const __nv_bfloat16* x;  // kQX: the activation, quantized on the way
     const __nv_bfloat16* bias;
     const __nv_bfloat16* bias2;
     const __nv_bfloat16* res;
@@ -91,19 +105,90 @@ struct RowsParams {
 
 __device__ __forceinline__ void record_status(uint32_t code) { atomicCAS(&g_rows_status, 0u, code); }
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr)
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr)
 {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
     return v;
 }
 
-template <int kKind, bool kGated, int kNT>
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// Quantizes rows x[0 .. M) of one stage (kKps columns from k0) into the stage's operand tile
+// (128-byte rows under the 128-byte swizzle) and scale atoms, with the activation quantizer's
+// arithmetic.  Four lanes take one MX block.  Blocks past K get zero codes and scales (the
+// MMA's other operand is zero there, and 0 x NaN must not reach the sum); tile rows past M are
+// left as they are, since they only reach output columns that nothing reads.
+template <int kKind>
+struct QuantX {
+    static constexpr int kKps = kKind == kMxf4 ? 256 : 128;
+    static constexpr int kLanes = kKps / 8;                // lanes a row
+    static constexpr int kRounds = 16 * kLanes / 128;      // of 128 threads, for 16 rows
+    uint4 raw[kRounds];
+
+    __device__ __forceinline__ void load(const RowsParams& p, int ks, int tid)
+    {
+#pragma unroll
+        for (int i = 0; i < kRounds; ++i) {
+            const int unit = i * 128 + tid, row = unit / kLanes, k = ks * kKps + unit % kLanes * 8;
+            raw[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (row < p.M && k < p.K) raw[i] = __ldg(reinterpret_cast<const uint4*>(p.x + static_cast<size_t>(row) * p.K + k));
+        }
+    }
+
+    __device__ __forceinline__ void store(const RowsParams& p, int ks, int tid, uint8_t* tile, uint8_t* sf) const
+    {
+        constexpr uint32_t kEmax = kKind == kMxf8 ? 8u : 2u;
+#pragma unroll
+        for (int i = 0; i < kRounds; ++i) {
+            const int unit = i * 128 + tid, row = unit / kLanes, kl = unit % kLanes * 8;
+            if ((i * 128 + (tid & ~31)) / kLanes >= p.M) break;  // warp-uniform: no row of this warp is live
+            const uint4 o = raw[i];
+            uint32_t m = absmax_bf16x2(absmax_bf16x2(o.x, o.y), absmax_bf16x2(o.z, o.w));
+            m = absmax_bf16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+            m = absmax_bf16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+            m = absmax_bf16x2(m, __byte_perm(m, 0, 0x1032));
+            const uint32_t sc = e8m0_code<kEmax>(m);
+            const float inv = e8m0_inverse(sc);
+            const uint32_t keep = sc == 255u ? 0u : 0xFFFFFFFFu;
+            const uint32_t w[4] = {o.x, o.y, o.z, o.w};
+            float q[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                q[2 * j] = lo_f(w[j]) * inv;
+                q[2 * j + 1] = hi_f(w[j]) * inv;
+            }
+            if (row < p.M) {
+                const uint32_t byte = static_cast<uint32_t>(kKind == kMxf8 ? kl : kl / 2);
+                uint8_t* at = tile + row * 128 + (((byte >> 4) ^ (static_cast<uint32_t>(row) & 7u)) << 4) + (byte & 15u);
+                if constexpr (kKind == kMxf8) {
+                    const uint32_t c0 = (cvt_e4m3x2(q[0], q[1]) | (cvt_e4m3x2(q[2], q[3]) << 16)) & keep;
+                    const uint32_t c1 = (cvt_e4m3x2(q[4], q[5]) | (cvt_e4m3x2(q[6], q[7]) << 16)) & keep;
+                    *reinterpret_cast<uint2*>(at) = make_uint2(c0, c1);
+                } else {
+                    *reinterpret_cast<uint32_t*>(at) = cvt_e2m1x8(q) & keep;
+                }
+                if ((tid & 3) == 0) sf[(kl / 128) * 512 + row * 16 + (kl / 32 & 3)] = static_cast<uint8_t>(sc);
+            }
+        }
+    }
+};
+
+template <int kKind, bool kGated, int kNT, bool kQX>
 __global__ void __launch_bounds__(kThreads, 2)
     gemm_rows_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_w2,
-                     const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_sfw,
-                     const __grid_constant__ CUtensorMap map_sfw2, const __grid_constant__ CUtensorMap map_sfx,
-                     const RowsParams p)
+                     const __grid_constant__ CUtensorMap map_x, const RowsParams p)
 {
     using C = Cfg<kKind, kGated, kNT>;
     constexpr int S = C::kStages;
@@ -114,66 +199,147 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
     uint64_t* empty = full + S;
-    uint64_t* acc_full = full + 2 * S;
-    uint32_t* tmem_base_smem = reinterpret_cast<uint32_t*>(full + 2 * S + 1);
+    uint64_t* sf_ready = full + 2 * S;  // a stage's scales are in TMEM (and so the stage has landed)
+    uint64_t* acc_full = full + 3 * S;
+    uint32_t* tmem_base_smem = reinterpret_cast<uint32_t*>(full + 3 * S + 1);
     uint32_t* failed = tmem_base_smem + 1;
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const int split = gridDim.x;  // the cluster: one CTA per range of K
+    const int split = gridDim.x;  // the cluster: one CTA per range of K (a power of two)
     const int rank = blockIdx.x;
     const int tile = blockIdx.y;
     const int ks0 = static_cast<int>(static_cast<int64_t>(p.k_stages) * rank / split);
     const int ks1 = static_cast<int>(static_cast<int64_t>(p.k_stages) * (rank + 1) / split);
+    const int n_stages = ks1 - ks0;
+    const int n_first = min(S, n_stages);  // the ring starts out empty
+    // debug: leave one stage unfilled, so that the MMA wait runs out
+    const int skipped = (p.debug & 1u) && rank == 0 && tile == 0 ? 0 : -1;
 
+    // one operand's scale bytes in the CTA's stage `it` (the last stage of K may have fewer atoms)
+    auto sf_bytes_of = [&](int it) {
+        const int a0 = (ks0 + it) * C::kAtoms;
+        return static_cast<uint32_t>(min(C::kAtoms, static_cast<int>(p.atoms_k) - a0)) * 512u;
+    };
+    // operand o's scales (0, 1: the weights; kW: the activation) of a stage: one contiguous run
+    auto load_sf = [&](int o, int it) {
+        const uint8_t* base = o == C::kW ? p.sf_x : o == 0 ? p.sf_w : p.sf_w2;
+        const size_t row = o == C::kW ? 0 : static_cast<size_t>(tile) * p.atoms_k * 512u;
+        bulk_load(smem + C::kOffSf + (o * S + it % S) * C::kSf, base + row + static_cast<size_t>(ks0 + it) * C::kSf,
+                  sf_bytes_of(it), smem_u32(&full[it % S]));
+    };
+    constexpr int kSfOps = C::kW + (kQX ? 0 : 1);  // operands whose scales are loaded
+    auto expect = [&](int it) {
+        mbar_arrive_expect_tx(&full[it % S], C::kTxW + (kQX ? 0u : C::kTileX) +
+                                                 (kKind != kBf16 ? kSfOps * sf_bytes_of(it) : 0u));
+    };
+    auto load_w = [&](int it, uint64_t pol) {
+        uint8_t* st = smem + it % S * C::kStage;
+        const uint32_t bar = smem_u32(&full[it % S]);
+        const int kx = (ks0 + it) * (kKind == kBf16 ? 64 : 128);  // map elements (bytes, nibbles or bf16)
+        tma_load_2d<1>(st, &map_w, kx, tile * 128, bar, pol);
+        if constexpr (kGated) tma_load_2d<1>(st + C::kTileW, &map_w2, kx, tile * 128, bar, pol);
+    };
+    auto load_x = [&](int it, uint64_t pol) {
+        tma_load_2d<1>(smem + it % S * C::kStage + C::kOffX, &map_x, (ks0 + it) * (kKind == kBf16 ? 64 : 128), 0,
+                       smem_u32(&full[it % S]), pol);
+    };
+
+    uint64_t pol = 0;
     if (warp == 0 && lane == 0) {
-        for (int s = 0; s < S; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
-        }
-        mbar_init(acc_full, 1);
-        *failed = 0u;
+        for (int s = 0; s < S; ++s) mbar_init(&full[s], 1 + (kQX ? 4 : 0));  // the copies, and the quantizing warps
         fence_mbar_init();
+        pol = policy_evict_normal();
+        if (!p.early) grid_wait();
+        for (int it = 0; it < n_first; ++it) {
+            if (it == skipped) continue;
+            expect(it);
+            load_w(it, pol);
+            if constexpr (kKind != kBf16)
+                for (int o = 0; o < C::kW; ++o) load_sf(o, it);
+        }
     }
     if (warp == 1) {
         tmem_alloc<1>(tmem_base_smem, C::kTmem);
         tmem_relinquish<1>();
     }
+    if (warp == 2 && lane == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(&empty[s], 1);
+            mbar_init(&sf_ready[s], 2);  // the weights' scales, and the activation's
+        }
+        mbar_init(acc_full, 1);
+        *failed = 0u;
+        fence_mbar_init();
+    }
+    if (warp == 3 && lane == 0) {
+        prefetch_tmap(&map_w);
+        if (kGated) prefetch_tmap(&map_w2);
+        if (!kQX) prefetch_tmap(&map_x);
+    }
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_base_smem;
 
+    const int nq = tile * 128 + (warp & 3) * 32;  // the 32 output columns this warp finishes
+    const int n = nq + lane;
+    const bool live = n < p.N;
+    // Tokens are finished in fours: four a by rank a % split, its warps 0-3 and 4-7 taking
+    // alternate ones of the rank's.  first4: this warp's first four.
+    const int first4 = rank + split * (warp >> 2);
+    float b0 = 0.0f, b1 = 0.0f, gate4[4], res4[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        gate4[i] = 1.0f;
+        res4[i] = 0.0f;
+    }
+    // gate and residual of a four of tokens
+    auto load_four = [&](int a) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int t = 4 * a + i;
+            if (kGated || !live || t >= p.M) continue;
+            if (p.gate != nullptr) {
+                const size_t gi = static_cast<size_t>(static_cast<uint32_t>(t) / p.rows_per_group) * p.N + n;
+                gate4[i] = p.gate_f32 ? __ldg(static_cast<const float*>(p.gate) + gi)
+                                      : __bfloat162float(static_cast<const __nv_bfloat16*>(p.gate)[gi]);
+            }
+            if (p.res != nullptr) res4[i] = __bfloat162float(p.res[static_cast<size_t>(t) * p.N + n]);
+        }
+    };
+    // what the last step needs from memory, fetched while the weight streams
+    auto load_epilogue = [&]() {
+        if (!live || 4 * first4 >= p.M) return;
+        if (p.bias != nullptr) b0 = __bfloat162float(p.bias[n]);
+        if (kGated && p.bias2 != nullptr) b1 = __bfloat162float(p.bias2[n]);
+        load_four(first4);
+    };
+
     if (warp == 0) {
         if (lane == 0) {
-            const uint64_t pol = policy_evict_normal();
-            int it = 0;
             bool ok = true;
-            int64_t skipped = -1;
-            for (int ks = ks0; ks < ks1; ++ks, ++it) {
-                const int s = it % S;
-                if (!mbar_wait(&empty[s], ((it / S) & 1) ^ 1, kWaitNs)) {
+            if (p.early) grid_wait();
+            grid_launch_dependents();  // after the wait: see the head of the file
+            if constexpr (!kQX) {
+                for (int it = 0; it < n_first; ++it) {
+                    if (it == skipped) continue;
+                    load_x(it, pol);
+                    if constexpr (kKind != kBf16) load_sf(C::kW, it);
+                }
+            }
+            int it = n_first;
+            for (; it < n_stages; ++it) {
+                if (!mbar_wait(&empty[it % S], ((it / S) & 1) ^ 1, kWaitNs)) {
                     ok = false;
                     break;
                 }
-                if ((p.debug & 1u) && it == 0 && rank == 0 && tile == 0) {
-                    skipped = 0;  // deliberately leave the stage unfilled: the MMA wait runs out
-                    continue;
-                }
-                uint8_t* st = smem + s * C::kStage;
-                uint8_t* sf = smem + C::kOffSf + s * (C::kW + 1) * C::kSf;
-                const uint32_t bar = smem_u32(&full[s]);
-                const int kx = kKind == kBf16 ? ks * 64 : ks * 128;  // map elements (bytes, nibbles or bf16)
-                mbar_arrive_expect_tx(&full[s], C::kTx);
-                tma_load_2d<1>(st, &map_w, kx, tile * 128, bar, pol);
-                if constexpr (kGated) tma_load_2d<1>(st + C::kTileW, &map_w2, kx, tile * 128, bar, pol);
-                tma_load_2d<1>(st + C::kOffX, &map_x, kx, 0, bar, pol);
-                if constexpr (kKind != kBf16) {
-                    const int ka = ks * C::kAtoms * 128;  // 32-bit words of the scale rows
-                    tma_load_2d<1>(sf, &map_sfw, ka, tile, bar, pol);
-                    if constexpr (kGated) tma_load_2d<1>(sf + C::kSf, &map_sfw2, ka, tile, bar, pol);
-                    tma_load_2d<1>(sf + C::kW * C::kSf, &map_sfx, ka, 0, bar, pol);
-                }
+                expect(it);
+                load_w(it, pol);
+                if constexpr (!kQX) load_x(it, pol);
+                if constexpr (kKind != kBf16)
+                    for (int o = 0; o < kSfOps; ++o) load_sf(o, it);
             }
             // every copy issued has landed before this CTA may leave or reuse its memory
             for (int i = max(0, it - S); i < it; ++i)
@@ -183,6 +349,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 *failed = 1u;
             }
         }
+        __syncwarp();
     } else if (warp == 1) {
         if (lane == 0) {
             constexpr uint32_t fw = kKind == kMxf8 ? 5u : 1u;  // weight: E2M1 in both kinds
@@ -191,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             uint32_t s = 0, ph = 0;
             bool ok = true;
             for (int ks = ks0; ks < ks1; ++ks) {
-                if (!mbar_wait(&full[s], ph, kWaitNs)) {
+                if (!mbar_wait(kKind == kBf16 ? &full[s] : &sf_ready[s], ph, kWaitNs)) {
                     record_status(MXQ_ERR_TIMEOUT);
                     *failed = 1u;
                     ok = false;
@@ -199,12 +366,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
                 tc_fence_after();
                 const uint32_t st = smem_u32(smem + s * C::kStage);
-                const uint32_t sf = smem_u32(smem + C::kOffSf + s * (C::kW + 1) * C::kSf);
                 const uint32_t w_lo = sdesc_sw128_lo(st), x_lo = sdesc_sw128_lo(st + C::kOffX);
-                const uint32_t tsf = tmem + C::kSfCol;
-#pragma unroll
-                for (int a = 0; a < (C::kW + 1) * C::kAtoms; ++a)
-                    tc_copy_sf_atom<1>(tsf + 4 * a, sdesc_sf_atom(sf + a * 512));
+                const uint32_t tsf = tmem + C::kSfCol + s * C::kSfCols;
                 const int kvalid = p.K - ks * C::kKps;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -234,13 +397,62 @@ __global__ void __launch_bounds__(kThreads, 2)
                 *failed = 1u;
             }
         }
+        __syncwarp();
+    } else {
+        grid_wait();
+        load_epilogue();
+        if (kKind != kBf16 && warp < 4 && lane == 0) {
+            uint32_t s = 0, ph = 0;
+            for (int ks = ks0; ks < ks1; ++ks) {
+                // the stage's columns are free: it was refilled after its last MMAs completed
+                if (!mbar_wait(&full[s], ph, kWaitNs)) {
+                    record_status(MXQ_ERR_TIMEOUT);
+                    *failed = 1u;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t tsf = tmem + C::kSfCol + s * C::kSfCols;
+#pragma unroll
+                for (int o = 0; o < C::kW + 1; ++o)
+#pragma unroll
+                    for (int a = 0; a < C::kAtoms && (o == C::kW) == (warp == 3); ++a)
+                        tc_copy_sf_atom<1>(tsf + 4 * (o * C::kAtoms + a),
+                                           sdesc_sf_atom(smem_u32(smem + C::kOffSf + (o * S + s) * C::kSf + a * 512)));
+                tc_commit<1>(&sf_ready[s]);
+                if (++s == S) { s = 0; ph ^= 1; }
+            }
+        }
+        if constexpr (kQX) {
+            if (warp >= 4) {
+                const int tid = static_cast<int>(threadIdx.x) - 128;
+                QuantX<kKind> qx;
+                qx.load(p, ks0, tid);
+                for (int ks = ks0, it = 0; ks < ks1; ++ks, ++it) {
+                    const QuantX<kKind> cur = qx;
+                    if (ks + 1 < ks1) qx.load(p, ks + 1, tid);  // on its way during this stage
+                    const int s = it % S;
+                    if (!__all_sync(0xFFFFFFFFu, mbar_wait(&empty[s], ((it / S) & 1) ^ 1, kWaitNs))) {
+                        if (lane == 0) {
+                            record_status(MXQ_ERR_TIMEOUT);
+                            *failed = 1u;
+                        }
+                        break;
+                    }
+                    cur.store(p, ks, tid, smem + s * C::kStage + C::kOffX, smem + C::kOffSf + (C::kW * S + s) * C::kSf);
+                    fence_async_smem();  // the tensor core reads the stage through the async proxy
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&full[s]);
+                }
+            }
+        }
+        __syncwarp();
     }
-    // all MMAs are done and all copies landed; the stages' memory now holds the partials
-    __syncwarp();
+    // all MMAs are done and all copies landed
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    float* part = reinterpret_cast<float*>(smem);  // [kW][kNT][128]
+    // this CTA's partials, [kW][four of tokens][128 rows][4]
+    float4* part = reinterpret_cast<float4*>(smem);
     if (warp >= 4) {
         const int q = warp & 3;  // TMEM lane quarter this warp may access
 #pragma unroll
@@ -253,8 +465,10 @@ __global__ void __launch_bounds__(kThreads, 2)
                 tmem_ld_wait();
                 tmem_regs_ready(r);
 #pragma unroll
-                for (int t = 0; t < 16; ++t)
-                    if (t0 + t < p.M) part[(w * kNT + t0 + t) * 128 + q * 32 + lane] = __uint_as_float(r[t]);
+                for (int i = 0; i < 4; ++i)
+                    part[(w * (kNT / 4) + t0 / 4 + i) * 128 + q * 32 + lane] =
+                        make_float4(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1]),
+                                    __uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3]));
             }
         tc_fence_before();
     }
@@ -262,82 +476,87 @@ __global__ void __launch_bounds__(kThreads, 2)
     tc_fence_after();
     if (warp == 1) tmem_dealloc<1>(tmem, C::kTmem);
 
-    bool ok = true;
-    const uint32_t flag = smem_u32(failed);
-    const uint32_t mine = smem_u32(part);
-    for (int r = 0; r < split; ++r) {
-        const float f = ld_cluster_f32(mapa_shared(flag, r));
-        ok = ok && __float_as_uint(f) == 0u;
+    uint32_t bad = 0u;
+#pragma unroll
+    for (int r = 0; r < kMaxSplit; ++r)
+        if (r < split) bad |= ld_cluster_u32(mapa_shared(smem_u32(failed), r));
+    const int fours = (p.M + 3) / 4;
+    if (warp < 2) {  // these two had other work until now
+        grid_wait();
+        load_epilogue();
     }
-    if (ok) {
-        const int nq = tile * 128 + (warp & 3) * 32;  // this warp's 32 output columns
-        const int n = nq + lane;
-        const bool live = n < p.N;
-        const float b0 = p.bias != nullptr && live ? __bfloat162float(p.bias[n]) : 0.0f;
-        const float b1 = kGated && p.bias2 != nullptr && live ? __bfloat162float(p.bias2[n]) : 0.0f;
+    if (bad != 0u || first4 >= fours) cluster_arrive();  // nothing (more) to read from the peers
+    if (bad == 0u)
         with_act(p.act, [&](auto act) {
-            for (int t = rank + split * (warp >> 2); t < p.M; t += split * 2) {
-                float v[C::kW];
+            for (int a = first4; a < fours; a += split * 2) {
+                float4 v[C::kW];
 #pragma unroll
                 for (int w = 0; w < C::kW; ++w) {
-                    const uint32_t off = ((w * kNT + t) * 128 + (warp & 3) * 32 + lane) * 4;
-                    float a[kMaxSplit];
+                    const uint32_t at = smem_u32(part + (w * (kNT / 4) + a) * 128 + (warp & 3) * 32 + lane);
+                    float4 f[kMaxSplit];
 #pragma unroll
                     for (int r = 0; r < kMaxSplit; ++r)
-                        a[r] = r < split ? ld_cluster_f32(mapa_shared(mine + off, r)) : 0.0f;
-                    v[w] = a[0];
+                        f[r] = r < split ? ld_cluster_f32x4(mapa_shared(at, r)) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    v[w] = f[0];
 #pragma unroll
-                    for (int r = 1; r < kMaxSplit; ++r) v[w] += a[r];
-                }
-                float o = act_f32<act>(v[0] + b0);
-                if constexpr (kGated) {
-                    o *= v[C::kW - 1] + b1;
-                } else {
-                    if (p.gate != nullptr && live) {
-                        const size_t gi = static_cast<size_t>(static_cast<uint32_t>(t) / p.rows_per_group) * p.N + n;
-                        o *= p.gate_f32 ? static_cast<const float*>(p.gate)[gi]
-                                        : __bfloat162float(static_cast<const __nv_bfloat16*>(p.gate)[gi]);
-                    }
-                    if (p.res != nullptr && live) o += __bfloat162float(p.res[static_cast<size_t>(t) * p.N + n]);
-                }
-                if (!kGated || p.out_fmt == MXQ_OUT_BF16) {
-                    if (live) p.y[static_cast<size_t>(t) * p.N + n] = __float2bfloat16_rn(o);
-                    continue;
-                }
-                // h: the warp's 32 values of this token are one MX block (N is a multiple of 32)
-                uint32_t sc = 0u;
-                if (nq < p.N) {
-                    const uint32_t hb = bf16x2_bits(o, o);
-                    const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, hb & 0x7FFFu);
-                    const bool e4m3 = p.out_fmt == MXQ_FMT_E4M3;
-                    sc = e4m3 ? e8m0_code<8u>(m) : e8m0_code<2u>(m);
-                    const float q = lo_f(hb) * e8m0_inverse(sc);
-                    const float q1 = __shfl_down_sync(0xFFFFFFFFu, q, 1);
-                    if (e4m3) {
-                        p.q_codes[static_cast<size_t>(t) * p.N + n] =
-                            sc == 255u ? uint8_t(0) : static_cast<uint8_t>(cvt_e4m3x2(q, 0.0f) & 0xFFu);
-                    } else if ((lane & 1) == 0) {
-                        const float pair[8] = {q, q1, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                        p.q_codes[(static_cast<size_t>(t) * p.N + n) / 2] =
-                            sc == 255u ? uint8_t(0) : static_cast<uint8_t>(cvt_e2m1x8(pair) & 0xFFu);
+                    for (int r = 1; r < kMaxSplit; ++r) {
+                        v[w].x += f[r].x;
+                        v[w].y += f[r].y;
+                        v[w].z += f[r].z;
+                        v[w].w += f[r].w;
                     }
                 }
-                if (lane == 0)  // this token's scale byte (0 for the padding past N)
-                    p.q_sf[sf_word(t, tile, p.atoms_n) + (warp & 3)] = static_cast<uint8_t>(sc);
+                // the peers may leave once the last four has been read; what follows is local
+                if (a + split * 2 >= fours) cluster_arrive();
+                if (a != first4) load_four(a);
+                const float s0[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+                [[maybe_unused]] const float s1[4] = {v[C::kW - 1].x, v[C::kW - 1].y, v[C::kW - 1].z, v[C::kW - 1].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int t = 4 * a + i;
+                    if (t >= p.M) break;
+                    float o = act_f32<act>(s0[i] + b0);
+                    if constexpr (kGated) o *= s1[i] + b1;
+                    else o = fmaf(o, gate4[i], res4[i]);
+                    if (!kGated || p.out_fmt == MXQ_OUT_BF16) {
+                        if (live) p.y[static_cast<size_t>(t) * p.N + n] = __float2bfloat16_rn(o);
+                        continue;
+                    }
+                    // h: the warp's 32 values of this token are one MX block (N is a multiple of 32)
+                    uint32_t sc = 0u;
+                    if (nq < p.N) {
+                        const uint32_t hb = bf16x2_bits(o, o);
+                        const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, hb & 0x7FFFu);
+                        const bool e4m3 = p.out_fmt == MXQ_FMT_E4M3;
+                        sc = e4m3 ? e8m0_code<8u>(m) : e8m0_code<2u>(m);
+                        const float q = lo_f(hb) * e8m0_inverse(sc);
+                        const float q1 = __shfl_down_sync(0xFFFFFFFFu, q, 1);
+                        if (e4m3) {
+                            p.q_codes[static_cast<size_t>(t) * p.N + n] =
+                                sc == 255u ? uint8_t(0) : static_cast<uint8_t>(cvt_e4m3x2(q, 0.0f) & 0xFFu);
+                        } else if ((lane & 1) == 0) {
+                            const float pair[8] = {q, q1, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                            p.q_codes[(static_cast<size_t>(t) * p.N + n) / 2] =
+                                sc == 255u ? uint8_t(0) : static_cast<uint8_t>(cvt_e2m1x8(pair) & 0xFFu);
+                        }
+                    }
+                    if (lane == 0)  // this token's scale byte (0 for the padding past N)
+                        p.q_sf[sf_word(t, tile, p.atoms_n) + (warp & 3)] = static_cast<uint8_t>(sc);
+                }
             }
         });
-        if (kGated && p.out_fmt != MXQ_OUT_BF16)  // the layout's padding rows, one word of this tile each
-            for (int t = p.M + rank * kThreads + static_cast<int>(threadIdx.x); t < 128; t += split * kThreads)
-                *reinterpret_cast<uint32_t*>(p.q_sf + sf_word(t, tile, p.atoms_n)) = 0u;
-    }
-    cluster_sync();  // no CTA leaves while another may read its partials
+    // the layout's padding rows, one word of this tile each
+    if (kGated && p.out_fmt != MXQ_OUT_BF16 && rank == 0 && bad == 0u)
+        for (int t = p.M + static_cast<int>(threadIdx.x); t < 128; t += kThreads)
+            *reinterpret_cast<uint32_t*>(p.q_sf + sf_word(t, tile, p.atoms_n)) = 0u;
+    cluster_wait();  // no CTA leaves while another may read its partials
 }
 
-template <int kKind, bool kGated, int kNT>
-cudaError_t launch_rows(const CUtensorMap (&m)[6], const RowsParams& p, int split, int tiles, cudaStream_t stream)
+template <int kKind, bool kGated, int kNT, bool kQX>
+cudaError_t launch_rows(const CUtensorMap (&m)[3], const RowsParams& p, int split, int tiles, cudaStream_t stream)
 {
     using C = Cfg<kKind, kGated, kNT>;
-    auto kern = gemm_rows_kernel<kKind, kGated, kNT>;
+    auto kern = gemm_rows_kernel<kKind, kGated, kNT, kQX>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -345,27 +564,31 @@ cudaError_t launch_rows(const CUtensorMap (&m)[6], const RowsParams& p, int spli
     cfg.blockDim = dim3(kThreads, 1, 1);
     cfg.dynamicSmemBytes = C::kSmem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = split;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, m[0], m[1], m[2], m[3], m[4], m[5], p);
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, m[0], m[1], m[2], p);
 }
 
 template <int kKind, bool kGated>
-cudaError_t launch_nt(int nt, const CUtensorMap (&m)[6], const RowsParams& p, int split, int tiles,
+cudaError_t launch_nt(int nt, const CUtensorMap (&m)[3], const RowsParams& p, int split, int tiles,
                       cudaStream_t stream)
 {
-    if (nt == 16) return launch_rows<kKind, kGated, 16>(m, p, split, tiles, stream);
-    if (nt == 32) return launch_rows<kKind, kGated, 32>(m, p, split, tiles, stream);
-    return launch_rows<kKind, kGated, 64>(m, p, split, tiles, stream);
+    if constexpr (kKind != kBf16)
+        if (p.x != nullptr) return launch_rows<kKind, kGated, 16, true>(m, p, split, tiles, stream);
+    if (nt == 16) return launch_rows<kKind, kGated, 16, false>(m, p, split, tiles, stream);
+    if (nt == 32) return launch_rows<kKind, kGated, 32, false>(m, p, split, tiles, stream);
+    return launch_rows<kKind, kGated, 64, false>(m, p, split, tiles, stream);
 }
 
 template <int kKind>
-cudaError_t launch_kind(bool gated, int nt, const CUtensorMap (&m)[6], const RowsParams& p, int split, int tiles,
+cudaError_t launch_kind(bool gated, int nt, const CUtensorMap (&m)[3], const RowsParams& p, int split, int tiles,
                         cudaStream_t stream)
 {
     return gated ? launch_nt<kKind, true>(nt, m, p, split, tiles, stream)
@@ -389,10 +612,7 @@ int launch_gemm_rows(const GemmArgs& g, cudaStream_t stream, const char** msg, c
     const bool gated = g.epilogue == kEpilogueGated;
     const int kind = g.bf16 ? kBf16 : g.a_fmt == kFmtE4M3 ? kMxf8 : kMxf4;
     const int nt = g.M <= 16 ? 16 : g.M <= 32 ? 32 : 64;
-    const int64_t atoms_k = sf_atoms_k(g.K);
-    const uint32_t ak = kind == kMxf4 ? 2 : 1;
-    CUtensorMap m[6];
-    bool ok = true;
+    CUtensorMap m[3];
     auto weight = [&](CUtensorMap* t, const void* w) {
         if (kind == kBf16)
             return make_map_2d(t, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, w, g.K, g.N, g.K * 2, 64, 128,
@@ -403,26 +623,18 @@ int launch_gemm_rows(const GemmArgs& g, cudaStream_t stream, const char** msg, c
         return make_map_2d(t, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, g.K / 2, g.N, g.K / 2, 128, 128,
                            CU_TENSOR_MAP_SWIZZLE_128B);
     };
-    auto scales = [&](CUtensorMap* t, const void* sf, int64_t rows) {
-        return make_map_2d(t, CU_TENSOR_MAP_DATA_TYPE_UINT32, sf, atoms_k * 128, ceil_div(rows, 128), atoms_k * 512,
-                           ak * 128, 1, CU_TENSOR_MAP_SWIZZLE_NONE);
-    };
-    ok = weight(&m[0], g.w_codes);
+    bool ok = weight(&m[0], g.w_codes);
     if (gated) ok = ok && weight(&m[1], g.w2_codes);
-    else m[1] = m[0];
-    if (kind == kBf16) {
+    else m[1] = m[0];  // never used
+    const uint64_t row = kind == kMxf8 ? g.K : g.K / 2;
+    if (g.x != nullptr)
+        m[2] = m[0];  // never used: x is quantized inside the kernel
+    else if (kind == kBf16)
         ok = ok && make_map_2d(&m[2], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, g.a_codes, g.K, g.M, g.K * 2, 64, nt,
                                CU_TENSOR_MAP_SWIZZLE_128B);
-        m[3] = m[4] = m[5] = m[0];  // never used
-    } else {
-        const uint64_t row = kind == kMxf8 ? g.K : g.K / 2;
+    else
         ok = ok && make_map_2d(&m[2], CU_TENSOR_MAP_DATA_TYPE_UINT8, g.a_codes, row, g.M, row, 128, nt,
                                CU_TENSOR_MAP_SWIZZLE_128B);
-        ok = ok && scales(&m[3], g.w_sf, g.N);
-        if (gated) ok = ok && scales(&m[4], g.w2_sf, g.N);
-        else m[4] = m[3];
-        ok = ok && scales(&m[5], g.a_sf, g.M);
-    }
     if (!ok) {
         *msg = "cuTensorMapEncodeTiled failed (driver entry point unavailable or invalid operand layout)";
         return MXQ_ERR_CUDA;
@@ -438,6 +650,12 @@ int launch_gemm_rows(const GemmArgs& g, cudaStream_t stream, const char** msg, c
     p.rows_per_group = static_cast<uint32_t>(std::min<int64_t>(g.rows_per_group, g.M));
     p.atoms_n = static_cast<uint32_t>(sf_atoms_k(g.N));
     p.debug = debug_flags();
+    p.sf_w = static_cast<const uint8_t*>(g.w_sf);
+    p.sf_w2 = static_cast<const uint8_t*>(g.w2_sf);
+    p.sf_x = static_cast<const uint8_t*>(g.a_sf);
+    p.atoms_k = static_cast<uint32_t>(sf_atoms_k(g.K));
+    p.early = g.early ? 1 : 0;
+    p.x = static_cast<const __nv_bfloat16*>(g.x);
     p.bias = static_cast<const __nv_bfloat16*>(g.bias);
     p.bias2 = static_cast<const __nv_bfloat16*>(g.bias2);
     p.res = static_cast<const __nv_bfloat16*>(g.residual);
@@ -462,7 +680,7 @@ int launch_gemm_rows(const GemmArgs& g, cudaStream_t stream, const char** msg, c
         return MXQ_ERR_CUDA;
     }
     if (path)
-        snprintf(path, path_len, "rows %s 128x%d split %d tiles %d%s", kind == kBf16 ? "bf16" : kind == kMxf8 ? "mxf8f6f4" : "mxf4",
+        snprintf(path, path_len, "rows%s %s 128x%d split %d tiles %d%s", g.x ? " +quantize x" : "", kind == kBf16 ? "bf16" : kind == kMxf8 ? "mxf8f6f4" : "mxf4",
                  nt, split, tiles, epilogue_name(g));
     return MXQ_OK;
 }

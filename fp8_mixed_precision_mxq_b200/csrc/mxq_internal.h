@@ -99,6 +99,11 @@ struct GemmArgs {
     const void* w2_codes = nullptr;
     const void* w2_sf = nullptr;
     const void* bias2 = nullptr;
+    // few-row kernel only.  x: the activation in bf16 (M <= kRowsMaxQuantM), quantized to a_fmt
+    // inside the kernel; a_codes and a_sf are not read.  early: the kernel before on the stream
+    // is this library's, launched behind everything that wrote the weight.
+    const void* x = nullptr;
+    bool early = false;
 };
 
 // Builds the tensor maps and launches the tcgen05 GEMM.  Returns an mxq_status;
@@ -110,6 +115,7 @@ const char* epilogue_name(const GemmArgs& g);  // for the path description
 // The residual or gated GEMM for at most kRowsMaxM activation rows (gemm_rows.cu); arguments
 // and results as launch_gemm's.
 constexpr int64_t kRowsMaxM = 64;
+constexpr int64_t kRowsMaxQuantM = 16;
 int launch_gemm_rows(const GemmArgs& g, cudaStream_t stream, const char** msg, char* path, size_t path_len);
 
 // Device status words written by kernels whose bounded waits ran out (the GEMMs' and

@@ -12,10 +12,9 @@
 // row in registers (first the mean, then the centered squares), so a large common offset
 // costs no digits.
 //
-// One CTA per row, the row in registers (C chunks of 8 channels a thread): x and y are read
-// once and z and h written once, which is all the traffic there is; HBM bounds it.  The
-// per-channel vectors (gate, scale, shift, weights) are shared by all rows of a group and
-// come from L1.
+// A CTA holds its rows in registers: x and y are read once and z and h written once, which is
+// all the traffic there is; HBM bounds it.  The per-channel vectors (gate, scale, shift, weights)
+// are shared by all rows of a group and come from L1.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -27,7 +26,18 @@ namespace mxq {
 
 namespace {
 
-constexpr int kMaxThreads = 512;
+constexpr int kMaxThreads = 1024, kMaxWarps = kMaxThreads / 32;
+
+// Registers a thread may take: what lets the most rows be under way on an SM without spilling the
+// row itself.  Measured at 32760 x 5120 (gate, scale and shift in fp32): one row of two chunks a
+// thread at 48 registers 240 us (bf16 out), at 56 269, at 40 273; two rows at 64 registers 284,
+// but with E4M3 out 559 us (75600 rows) against 591; an fp32 stream two rows at 80 registers 317
+// us, one row at 64 374.
+constexpr int norm_regs(bool f32, int c, int r, bool early)
+{
+    return early ? 128 : c * r < 4 ? (f32 ? 64 : 48) : f32 && c < 4 ? 80 : 64;
+}
+
 
 struct NormParams {
     const void* x;
@@ -43,306 +53,540 @@ struct NormParams {
     void* out;    // h in bf16, or the codes
     uint8_t* sf;  // tiled scales (quantized h)
     int64_t rows;
+    int64_t rows_pad;    // rows of the scale layout
+    int64_t row_blocks;  // CTAs that have rows; the rest write the layout's padding
+    int e4m3;            // a quantized h's format
     uint32_t K;
     uint32_t rows_per_group;
     uint32_t atoms_k;
     float eps;
     float inv_k;
     int norm, post;  // MXQ_NORM_*
-    int vec_f32;     // the per-channel vectors are fp32 (else bf16)
 };
 
-// Eight consecutive channels of a bf16 or fp32 array, as they lie in memory.
+// A thread's eight channels of a 256-channel span: four at 4 * lane and four at 128 + 4 * lane, so
+// that a warp's every load and store of fp32 or bf16 values is one contiguous run (eight
+// neighbouring channels a thread would spread an fp32 load over twice its cache lines, which the
+// L1 pipe felt: 70 % busy).  w: the values as they lie in memory.
+template <bool kF32>
 struct Raw8 {
-    uint4 a, b;
+    uint4 w[kF32 ? 2 : 1];
 };
 
-__device__ __forceinline__ Raw8 load_vec8(const void* p, size_t i, bool f32)
+// at: the channels of the two fours.
+struct At {
+    uint32_t a, b;
+};
+
+template <bool kF32, class T>
+__device__ __forceinline__ T* at4(T* p, size_t i)
 {
-    Raw8 r;
-    if (f32) {
-        const uint4* q = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + i);
-        r.a = __ldg(q);
-        r.b = __ldg(q + 1);
-    } else {
-        r.a = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + i));
-        r.b = make_uint4(0u, 0u, 0u, 0u);
-    }
-    return r;
+    return p + i * (kF32 ? 4 : 2);
 }
 
-__device__ __forceinline__ void widen8(const Raw8& r, bool f32, float (&v)[8])
+// Channel vectors: shared by the rows, kept in L1.
+template <bool kF32>
+__device__ __forceinline__ Raw8<kF32> load_vec8(const void* p, size_t base, const At& at)
 {
-    if (f32) {
-        v[0] = __uint_as_float(r.a.x); v[1] = __uint_as_float(r.a.y);
-        v[2] = __uint_as_float(r.a.z); v[3] = __uint_as_float(r.a.w);
-        v[4] = __uint_as_float(r.b.x); v[5] = __uint_as_float(r.b.y);
-        v[6] = __uint_as_float(r.b.z); v[7] = __uint_as_float(r.b.w);
+    const uint8_t* q = at4<kF32>(static_cast<const uint8_t*>(p), base);
+    Raw8<kF32> r;
+    if constexpr (kF32) {
+        r.w[0] = __ldg(reinterpret_cast<const uint4*>(at4<true>(q, at.a)));
+        r.w[1] = __ldg(reinterpret_cast<const uint4*>(at4<true>(q, at.b)));
     } else {
-        v[0] = lo_f(r.a.x); v[1] = hi_f(r.a.x);
-        v[2] = lo_f(r.a.y); v[3] = hi_f(r.a.y);
-        v[4] = lo_f(r.a.z); v[5] = hi_f(r.a.z);
-        v[6] = lo_f(r.a.w); v[7] = hi_f(r.a.w);
+        const uint2 a = __ldg(reinterpret_cast<const uint2*>(at4<false>(q, at.a)));
+        const uint2 b = __ldg(reinterpret_cast<const uint2*>(at4<false>(q, at.b)));
+        r.w[0] = make_uint4(a.x, a.y, b.x, b.y);
     }
+    return r;
 }
 
 // The rows themselves are read once: streaming loads, which leave L1 to the vectors.
 template <bool kF32>
-__device__ __forceinline__ Raw8 load_row8(const void* p, size_t i)
+__device__ __forceinline__ Raw8<kF32> load_row8(const void* p, size_t base, const At& at)
 {
-    Raw8 r;
-    if (kF32) {
-        const uint4* q = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + i);
-        r.a = __ldcs(q);
-        r.b = __ldcs(q + 1);
+    const uint8_t* q = at4<kF32>(static_cast<const uint8_t*>(p), base);
+    Raw8<kF32> r;
+    if constexpr (kF32) {
+        r.w[0] = __ldcs(reinterpret_cast<const uint4*>(at4<true>(q, at.a)));
+        r.w[1] = __ldcs(reinterpret_cast<const uint4*>(at4<true>(q, at.b)));
     } else {
-        r.a = __ldcs(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + i));
-        r.b = make_uint4(0u, 0u, 0u, 0u);
+        const uint2 a = __ldcs(reinterpret_cast<const uint2*>(at4<false>(q, at.a)));
+        const uint2 b = __ldcs(reinterpret_cast<const uint2*>(at4<false>(q, at.b)));
+        r.w[0] = make_uint4(a.x, a.y, b.x, b.y);
     }
     return r;
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&v)[8])
+// live_a, live_b: whether the fours lie inside the row.
+template <bool kF32>
+__device__ __forceinline__ void store_row8(void* p, size_t base, const At& at, bool live_a, bool live_b,
+                                           const Raw8<kF32>& r)
 {
-    return make_uint4(bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3]), bf16x2_bits(v[4], v[5]), bf16x2_bits(v[6], v[7]));
-}
-
-// Sum over the CTA, the same value in every thread.  `red` is used by this call only.
-__device__ __forceinline__ float block_sum(float v, float* red)
-{
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    const int warps = blockDim.x >> 5;
-    if (warps == 1) return v;
-    const int lane = threadIdx.x & 31;
-    if (lane == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = lane < warps ? red[lane] : 0.0f;
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);  // at most 16 warps
-    return __shfl_sync(0xFFFFFFFFu, v, 0);
-}
-
-// Mean (0 for RMSNorm) and 1 / sqrt(variance + eps) of the CTA's row, whose channels past K
-// are held as zeros and masked out of the centered squares by `live`.
-template <int C>
-__device__ __forceinline__ float2 row_stats(const float (&v)[C][8], const bool (&live)[C], int kind, float inv_k,
-                                            float eps, float* red)
-{
-    float mean = 0.0f;
-    if (kind == MXQ_NORM_LAYER) {
-        float s = 0.0f;
-#pragma unroll
-        for (int j = 0; j < C; ++j)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) s += v[j][i];
-        mean = block_sum(s, red) * inv_k;
-    }
-    float q = 0.0f;
-#pragma unroll
-    for (int j = 0; j < C; ++j) {
-        if (!live[j]) continue;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float d = v[j][i] - mean;
-            q = fmaf(d, d, q);
-        }
-    }
-    const float var = block_sum(q, red + 16) * inv_k;
-    return make_float2(mean, __frsqrt_rn(var + eps));
-}
-
-// kF32: the residual stream x, z is fp32 (else bf16).  OUT: MXQ_OUT_BF16, MXQ_FMT_E2M1 or
-// MXQ_FMT_E4M3.  C: chunks of 8 channels per thread; chunk j of thread t is chunk j * T + t of
-// the row, so four neighbouring lanes hold one MX block.
-template <bool kF32, int OUT, int C>
-__global__ void __launch_bounds__(kMaxThreads) norm_residual_kernel(const NormParams p)
-{
-    __shared__ float red[64];
-    const int64_t row = blockIdx.x;
-    const uint32_t lane = threadIdx.x & 31u;
-    const uint32_t chunks = p.K / 8;
-    const bool vf = p.vec_f32 != 0;
-    if constexpr (OUT != MXQ_OUT_BF16) {
-        if (row >= p.rows) {  // a row of the scale layout's padding
-            for (uint32_t a = threadIdx.x; a < p.atoms_k; a += blockDim.x)
-                *reinterpret_cast<uint32_t*>(p.sf + sf_word(row, a, p.atoms_k)) = 0u;
-            return;
-        }
-    }
-    const size_t base = static_cast<size_t>(row) * p.K;
-    const size_t gbase = static_cast<size_t>(static_cast<uint32_t>(row) / p.rows_per_group) * p.K;
-
-    bool live[C];
-    uint32_t ch[C];  // first channel of each chunk
-    Raw8 xr[C], yr[C];
-    float v[C][8];   // the row: y (with a post norm), then z
-#pragma unroll
-    for (int j = 0; j < C; ++j) {
-        const uint32_t c = j * blockDim.x + threadIdx.x;
-        live[j] = c < chunks;
-        ch[j] = c * 8u;
-        xr[j].a = xr[j].b = yr[j].a = yr[j].b = make_uint4(0u, 0u, 0u, 0u);
-        if (live[j]) {
-            xr[j] = load_row8<kF32>(p.x, base + ch[j]);
-            if (p.y) yr[j] = load_row8<false>(p.y, base + ch[j]);
-        }
-    }
-    // up to two chunks a thread: the vectors of the last step are fetched here too, so that
-    // their latency passes beside the row's (a call of few rows is bound by nothing else)
-    constexpr bool kEarly = C <= 2;
-    Raw8 w_r[kEarly ? C : 1], b_r[kEarly ? C : 1], s_r[kEarly ? C : 1], t_r[kEarly ? C : 1];
-    if constexpr (kEarly) {
-#pragma unroll
-        for (int j = 0; j < C; ++j) {
-            if (!live[j]) continue;
-            if (p.weight) w_r[j] = load_vec8(p.weight, ch[j], vf);
-            if (p.bias) b_r[j] = load_vec8(p.bias, ch[j], vf);
-            if (p.scale) s_r[j] = load_vec8(p.scale, gbase + ch[j], vf);
-            if (p.shift) t_r[j] = load_vec8(p.shift, gbase + ch[j], vf);
-        }
-    }
-
-    if (p.y) {
-        float2 st = make_float2(0.0f, 1.0f);
-        if (p.post != MXQ_NORM_NONE) {
-#pragma unroll
-            for (int j = 0; j < C; ++j) widen8(yr[j], false, v[j]);
-            st = row_stats<C>(v, live, p.post, p.inv_k, p.eps, red + 32);
-        }
-#pragma unroll
-        for (int j = 0; j < C; ++j) {
-            float xv[8], t[8];
-            widen8(xr[j], kF32, xv);
-            widen8(yr[j], false, v[j]);
-            if (live[j]) {
-                if (p.post != MXQ_NORM_NONE) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) v[j][i] = (v[j][i] - st.x) * st.y;
-                    if (p.post_weight) {
-                        widen8(load_vec8(p.post_weight, ch[j], vf), vf, t);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) v[j][i] *= t[i];
-                    }
-                    if (p.post_bias) {
-                        widen8(load_vec8(p.post_bias, ch[j], vf), vf, t);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) v[j][i] += t[i];
-                    }
-                }
-                if (p.gate) {
-                    widen8(load_vec8(p.gate, gbase + ch[j], vf), vf, t);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) v[j][i] = fmaf(t[i], v[j][i], xv[i]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) v[j][i] += xv[i];
-                }
-                if constexpr (kF32) {
-                    float4* zp = reinterpret_cast<float4*>(static_cast<float*>(p.z) + base + ch[j]);
-                    zp[0] = make_float4(v[j][0], v[j][1], v[j][2], v[j][3]);
-                    zp[1] = make_float4(v[j][4], v[j][5], v[j][6], v[j][7]);
-                } else {
-                    Raw8 zr;
-                    zr.a = pack8(v[j]);
-                    zr.b = zr.a;
-                    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.z) + base + ch[j]) = zr.a;
-                    widen8(zr, false, v[j]);  // the norm sees the stored value
-                }
-            }
-        }
+    uint8_t* q = at4<kF32>(static_cast<uint8_t*>(p), base);
+    if constexpr (kF32) {
+        if (live_a) *reinterpret_cast<uint4*>(at4<true>(q, at.a)) = r.w[0];
+        if (live_b) *reinterpret_cast<uint4*>(at4<true>(q, at.b)) = r.w[1];
     } else {
-#pragma unroll
-        for (int j = 0; j < C; ++j) widen8(xr[j], kF32, v[j]);
-    }
-
-    const float2 st = row_stats<C>(v, live, p.norm, p.inv_k, p.eps, red);
-#pragma unroll
-    for (int j = 0; j < C; ++j) {
-        float t[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[j][i] = (v[j][i] - st.x) * st.y;
-        if (live[j]) {
-            if (p.weight) {
-                widen8(kEarly ? w_r[kEarly ? j : 0] : load_vec8(p.weight, ch[j], vf), vf, t);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[j][i] *= t[i];
-            }
-            if (p.bias) {
-                widen8(kEarly ? b_r[kEarly ? j : 0] : load_vec8(p.bias, ch[j], vf), vf, t);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[j][i] += t[i];
-            }
-            if (p.scale) {
-                widen8(kEarly ? s_r[kEarly ? j : 0] : load_vec8(p.scale, gbase + ch[j], vf), vf, t);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[j][i] = v[j][i] * (1.0f + t[i]);
-            }
-            if (p.shift) {
-                widen8(kEarly ? t_r[kEarly ? j : 0] : load_vec8(p.shift, gbase + ch[j], vf), vf, t);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[j][i] += t[i];
-            }
-        }
-        const uint4 o = pack8(v[j]);
-        if constexpr (OUT == MXQ_OUT_BF16) {
-            if (live[j]) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + base + ch[j]) = o;
-        } else {
-            // the quad's 32 values are one MX block: the activation quantizer's arithmetic on
-            // the bf16 h (scale from the abs-max's exponent field, codes rounded to nearest
-            // even with saturation, zero codes in a non-finite block)
-            constexpr uint32_t kEmax = OUT == MXQ_FMT_E4M3 ? 8u : 2u;
-            uint32_t m = absmax_bf16x2(absmax_bf16x2(o.x, o.y), absmax_bf16x2(o.z, o.w));
-            m = absmax_bf16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-            m = absmax_bf16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-            m = absmax_bf16x2(m, __byte_perm(m, 0, 0x1032));
-            const uint32_t sc = e8m0_code<kEmax>(m);
-            const float inv = e8m0_inverse(sc);
-            const uint32_t keep = sc == 255u ? 0u : 0xFFFFFFFFu;
-            // four blocks' scale bytes (16 lanes) make one word of the tiled layout
-            const uint32_t kb = ch[j] / 32u;
-            uint32_t word = live[j] ? sc << (8u * (kb & 3u)) : 0u;
-            word |= __shfl_xor_sync(0xFFFFFFFFu, word, 4);
-            word |= __shfl_xor_sync(0xFFFFFFFFu, word, 8);
-            float q[8];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t w = i == 0 ? o.x : i == 1 ? o.y : i == 2 ? o.z : o.w;
-                q[2 * i] = lo_f(w) * inv;
-                q[2 * i + 1] = hi_f(w) * inv;
-            }
-            if (live[j]) {
-                uint8_t* codes = static_cast<uint8_t*>(p.out);
-                if constexpr (OUT == MXQ_FMT_E2M1) {
-                    *reinterpret_cast<uint32_t*>(codes + (base + ch[j]) / 2) = cvt_e2m1x8(q) & keep;
-                } else {
-                    const uint32_t c0 = (cvt_e4m3x2(q[0], q[1]) | (cvt_e4m3x2(q[2], q[3]) << 16)) & keep;
-                    const uint32_t c1 = (cvt_e4m3x2(q[4], q[5]) | (cvt_e4m3x2(q[6], q[7]) << 16)) & keep;
-                    *reinterpret_cast<uint2*>(codes + base + ch[j]) = make_uint2(c0, c1);
-                }
-                // k-blocks past K inside the word stay 0, as the layout's padding requires
-                if ((lane & 15u) == 0) *reinterpret_cast<uint32_t*>(p.sf + sf_word(row, kb / 4u, p.atoms_k)) = word;
-            }
-        }
+        if (live_a) *reinterpret_cast<uint2*>(at4<false>(q, at.a)) = make_uint2(r.w[0].x, r.w[0].y);
+        if (live_b) *reinterpret_cast<uint2*>(at4<false>(q, at.b)) = make_uint2(r.w[0].z, r.w[0].w);
     }
 }
 
-template <bool kF32, int OUT>
-cudaError_t launch_c(int c, unsigned grid, int threads, const NormParams& p, cudaStream_t stream)
+// Values past the row's end are zeros.
+template <bool kF32>
+__device__ __forceinline__ void zero_dead(Raw8<kF32>& r, bool live_a, bool live_b)
 {
-    if (c == 1) norm_residual_kernel<kF32, OUT, 1><<<grid, threads, 0, stream>>>(p);
-    else if (c == 2) norm_residual_kernel<kF32, OUT, 2><<<grid, threads, 0, stream>>>(p);
-    else if (c <= 4) norm_residual_kernel<kF32, OUT, 4><<<grid, threads, 0, stream>>>(p);
-    else norm_residual_kernel<kF32, OUT, 8><<<grid, threads, 0, stream>>>(p);
-    return cudaGetLastError();
+    const uint4 o = make_uint4(0u, 0u, 0u, 0u);
+    if constexpr (kF32) {
+        if (!live_a) r.w[0] = o;
+        if (!live_b) r.w[1] = o;
+    } else {
+        if (!live_a) r.w[0].x = r.w[0].y = 0u;
+        if (!live_b) r.w[0].z = r.w[0].w = 0u;
+    }
 }
 
 template <bool kF32>
-cudaError_t launch_out(int out, int c, unsigned grid, int threads, const NormParams& p, cudaStream_t stream)
+__device__ __forceinline__ void widen8(const Raw8<kF32>& r, float2 (&v)[4])
 {
-    if (out == MXQ_FMT_E2M1) return launch_c<kF32, MXQ_FMT_E2M1>(c, grid, threads, p, stream);
-    if (out == MXQ_FMT_E4M3) return launch_c<kF32, MXQ_FMT_E4M3>(c, grid, threads, p, stream);
-    return launch_c<kF32, MXQ_OUT_BF16>(c, grid, threads, p, stream);
+    if constexpr (kF32) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            v[2 * i] = make_float2(__uint_as_float(r.w[i].x), __uint_as_float(r.w[i].y));
+            v[2 * i + 1] = make_float2(__uint_as_float(r.w[i].z), __uint_as_float(r.w[i].w));
+        }
+    } else {
+        v[0] = make_float2(lo_f(r.w[0].x), hi_f(r.w[0].x));
+        v[1] = make_float2(lo_f(r.w[0].y), hi_f(r.w[0].y));
+        v[2] = make_float2(lo_f(r.w[0].z), hi_f(r.w[0].z));
+        v[3] = make_float2(lo_f(r.w[0].w), hi_f(r.w[0].w));
+    }
+}
+
+// Stops the compiler from holding a packed chunk's widened values from one pass to the next.
+template <bool kF32>
+__device__ __forceinline__ void keep_packed(Raw8<kF32>& r)
+{
+    if constexpr (!kF32) asm volatile("" : "+r"(r.w[0].x), "+r"(r.w[0].y), "+r"(r.w[0].z), "+r"(r.w[0].w));
+}
+
+__device__ __forceinline__ uint4 pack8(const float2 (&v)[4])
+{
+    return make_uint4(bf16x2_bits(v[0].x, v[0].y), bf16x2_bits(v[1].x, v[1].y), bf16x2_bits(v[2].x, v[2].y),
+                      bf16x2_bits(v[3].x, v[3].y));
+}
+
+template <bool kF32>
+__device__ __forceinline__ void narrow8(const float2 (&v)[4], Raw8<kF32>& r)
+{
+    if constexpr (kF32) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            r.w[i] = make_uint4(__float_as_uint(v[2 * i].x), __float_as_uint(v[2 * i].y), __float_as_uint(v[2 * i + 1].x),
+                                __float_as_uint(v[2 * i + 1].y));
+    } else {
+        r.w[0] = pack8(v);
+    }
+}
+
+// Sums over the CTA, the same values in every thread.  `red` is used by this call only.
+template <int R>
+__device__ __forceinline__ void block_sum(float (&v)[R], float* red)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int r = 0; r < R; ++r) v[r] += __shfl_xor_sync(0xFFFFFFFFu, v[r], o);
+    const int warps = blockDim.x >> 5;
+    if (warps == 1) return;
+    const int lane = threadIdx.x & 31;
+    if (lane == 0)
+#pragma unroll
+        for (int r = 0; r < R; ++r) red[r * kMaxWarps + (threadIdx.x >> 5)] = v[r];
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        v[r] = lane < warps ? red[r * kMaxWarps + lane] : 0.0f;
+#pragma unroll
+        for (int o = kMaxWarps / 2; o > 0; o >>= 1) v[r] += __shfl_xor_sync(0xFFFFFFFFu, v[r], o);
+    }
+}
+
+// -mean (0 for RMSNorm) and 1 / sqrt(variance + eps) of the CTA's rows.  Channels past K (`live`
+// false; with kFull there are none) are held as zeros and left out of the centered squares.
+// load(r, j, t) gives chunk j of row r.
+template <int R, int C, bool kFull, class F>
+__device__ __forceinline__ void row_stats(F load, const bool (&live)[C][2], int kind, float inv_k, float eps,
+                                          float* red, float (&neg_mean)[R], float (&rstd)[R])
+{
+    float2 t[4];
+    if (kind == MXQ_NORM_LAYER) {
+        float s[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            float2 a = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int j = 0; j < C; ++j) {
+                load(r, j, t);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) a = __fadd2_rn(a, t[i]);
+            }
+            s[r] = a.x + a.y;
+        }
+        block_sum<R>(s, red);
+#pragma unroll
+        for (int r = 0; r < R; ++r) neg_mean[r] = -(s[r] * inv_k);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            float2 q = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int j = 0; j < C; ++j) {
+                load(r, j, t);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float m = kFull || live[j][i / 2] ? neg_mean[r] : 0.0f;
+                    const float2 d = __fadd2_rn(t[i], make_float2(m, m));
+                    q = __ffma2_rn(d, d, q);
+                }
+            }
+            rstd[r] = q.x + q.y;
+        }
+    } else {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            neg_mean[r] = 0.0f;
+            float2 q = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int j = 0; j < C; ++j) {
+                load(r, j, t);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) q = __ffma2_rn(t[i], t[i], q);
+            }
+            rstd[r] = q.x + q.y;
+        }
+    }
+    block_sum<R>(rstd, red + R * kMaxWarps);
+#pragma unroll
+    for (int r = 0; r < R; ++r) rstd[r] = __frsqrt_rn(rstd[r] * inv_k + eps);
+}
+
+struct Mul {
+    __device__ float2 operator()(float2 a, float2 t) const { return __fmul2_rn(a, t); }
+};
+struct Add {
+    __device__ float2 operator()(float2 a, float2 t) const { return __fadd2_rn(a, t); }
+};
+struct MulOnePlus {
+    __device__ float2 operator()(float2 a, float2 t) const
+    {
+        return __fmul2_rn(a, __fadd2_rn(t, make_float2(1.0f, 1.0f)));
+    }
+};
+
+// v = f(v, vector) on the threads' chunks of all rows, the vector from memory (`base`: of its
+// first channel) or already in registers.
+template <bool kVF32, int R, int C, class F>
+__device__ __forceinline__ void apply_vec(float2 (&v)[R][C][4], const void* from, size_t base, const At (&at)[C], F f)
+{
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+        float2 t[4];
+        widen8(load_vec8<kVF32>(from, base, at[j]), t);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[r][j][i] = f(v[r][j][i], t[i]);
+    }
+}
+
+template <bool kVF32, int R, int C, class F>
+__device__ __forceinline__ void apply_vec(float2 (&v)[R][C][4], const Raw8<kVF32> (&from)[C], F f)
+{
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+        float2 t[4];
+        widen8(from[j], t);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[r][j][i] = f(v[r][j][i], t[i]);
+    }
+}
+
+// v = (v + neg_mean) * rstd.
+template <int R, int C>
+__device__ __forceinline__ void normalize(float2 (&v)[R][C][4], const float (&neg_mean)[R], const float (&rstd)[R])
+{
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int j = 0; j < C; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[r][j][i] = __fmul2_rn(__fadd2_rn(v[r][j][i], make_float2(neg_mean[r], neg_mean[r])),
+                                        make_float2(rstd[r], rstd[r]));
+}
+
+// Writes one chunk of h: in bf16, or as MX codes and scale bytes.  c: its first channel.
+template <bool kQuant>
+__device__ __forceinline__ void emit(const NormParams& p, int64_t row, size_t base, uint32_t c, const At& at, bool live_a,
+                                     bool live_b, const float2 (&v)[4])
+{
+    Raw8<false> h;
+    narrow8(v, h);
+    if constexpr (!kQuant) {
+        store_row8(p.out, base, at, live_a, live_b, h);
+    } else {
+        // eight lanes' fours are one MX block (two, a and b): the activation quantizer's
+        // arithmetic on the bf16 h (scale from the abs-max's exponent field, codes rounded
+        // to nearest even with saturation, zero codes in a non-finite block)
+        const uint32_t ma = absmax_bf16x2(h.w[0].x, h.w[0].y), mb = absmax_bf16x2(h.w[0].z, h.w[0].w);
+        uint32_t m = absmax_bf16x2(__byte_perm(ma, mb, 0x5410), __byte_perm(ma, mb, 0x7632));  // a low, b high
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) m = absmax_bf16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        const uint32_t emax = p.e4m3 ? 8u : 2u;
+        const uint32_t ea = (m >> 7) & 255u, eb = (m >> 23) & 255u;
+        uint32_t sa = max(ea, emax) - emax, sb = max(eb, emax) - emax;
+        const float ia = __uint_as_float((254u - sa) << 23), ib = __uint_as_float((254u - sb) << 23);  // 2^(127 - s)
+        float2 q[4];
+        widen8(h, q);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q[i] = __fmul2_rn(q[i], i < 2 ? make_float2(ia, ia) : make_float2(ib, ib));
+        const bool nan_a = ea == 255u, nan_b = eb == 255u;
+        const bool odd = __any_sync(0xFFFFFFFFu, nan_a || nan_b);  // a non-finite block in the warp: rare
+        if (nan_a) sa = 255u;
+        if (nan_b) sb = 255u;
+        uint8_t* codes = static_cast<uint8_t*>(p.out);
+        if (p.e4m3) {
+            uint32_t ca = cvt_e4m3x2(q[0].x, q[0].y) | (cvt_e4m3x2(q[1].x, q[1].y) << 16);
+            uint32_t cb = cvt_e4m3x2(q[2].x, q[2].y) | (cvt_e4m3x2(q[3].x, q[3].y) << 16);
+            if (odd) {
+                if (nan_a) ca = 0u;
+                if (nan_b) cb = 0u;
+            }
+            if (live_a) *reinterpret_cast<uint32_t*>(codes + base + at.a) = ca;
+            if (live_b) *reinterpret_cast<uint32_t*>(codes + base + at.b) = cb;
+        } else {
+            const float f[8] = {q[0].x, q[0].y, q[1].x, q[1].y, q[2].x, q[2].y, q[3].x, q[3].y};
+            uint32_t e = cvt_e2m1x8(f);
+            if (odd) {
+                if (nan_a) e &= 0xFFFF0000u;
+                if (nan_b) e &= 0x0000FFFFu;
+            }
+            if (live_a) *reinterpret_cast<uint16_t*>(codes + (base + at.a) / 2) = static_cast<uint16_t>(e);
+            if (live_b) *reinterpret_cast<uint16_t*>(codes + (base + at.b) / 2) = static_cast<uint16_t>(e >> 16);
+        }
+        if ((threadIdx.x & 7u) == 0) {
+            // the blocks' scale bytes; k-blocks past K in the last atom are 0
+            uint8_t* sf = p.sf + sf_word(row, 0, p.atoms_k) + (c / 32u & 3u);
+            if (c < p.atoms_k * 128u) sf[(c / 128u) * 512u] = live_a ? static_cast<uint8_t>(sa) : uint8_t(0);
+            if (c + 128u < p.atoms_k * 128u) sf[(c / 128u) * 512u + 512u] = live_b ? static_cast<uint8_t>(sb) : uint8_t(0);
+        }
+    }
+}
+
+// A CTA takes R rows of one group.  kF32: the residual stream x, z is fp32 (else bf16); kVF32: so
+// are the channel vectors.  kQuant: h leaves as MX codes (else bf16).  C: chunks of 8 channels
+// per thread and row; chunk j of warp w is its lanes' part of span j * warps + w, whose MX blocks
+// lie in eight lanes each.  kFull: a row has exactly C * warps spans (else some channels are past
+// its end).  kEarly: the last step's vectors are fetched with the rows.
+// What keeps the kernel from the memory's rate is its own work, so: R rows share each vector's
+// loads and each barrier; arithmetic runs on packed fp32 pairs; a bf16 z is held packed between
+// the passes over it, which leaves registers for more rows on an SM; and each optional vector is
+// one branch around a loop over all the thread's values (tested chunk by chunk the options
+// became predicates, and a launch issued every option's instructions: 41 an element).  Many small
+// CTAs hide each other's barriers: persistent CTAs, with the next row prefetched into shared
+// memory, into L2 or into registers, all measured 20 to 60 % slower.
+// Measured (share of the copy rate): 32760 x 5120 with gate, scale, shift in fp32, bf16 out 241 us
+// (86 %), of an fp32 stream 318 us (98 %); 75600 x 5120 with E4M3 out 555 us (76 %).
+template <bool kF32, bool kVF32, bool kQuant, int C, int R, bool kFull, bool kEarly>
+__global__ void __maxnreg__(norm_regs(kF32, C, R, kEarly)) norm_residual_kernel(const NormParams p)
+{
+    __shared__ float red[4 * R * kMaxWarps];
+    const uint32_t lane = threadIdx.x & 31u;
+    const uint32_t per_group = (p.rows_per_group + R - 1) / R;  // CTAs a group
+    const uint32_t group = blockIdx.x / per_group;
+    const int64_t row0 = static_cast<int64_t>(group) * p.rows_per_group + (blockIdx.x - group * per_group) * R;
+    const int64_t group_end = min(static_cast<int64_t>(group + 1) * p.rows_per_group, p.rows);
+    if (row0 >= group_end) {
+        // CTAs past the rows take the rows of the scale layout's padding
+        const int64_t row = p.rows + (static_cast<int64_t>(blockIdx.x) - p.row_blocks);
+        if (kQuant && row >= p.rows && row < p.rows_pad)
+            for (uint32_t a = threadIdx.x; a < p.atoms_k; a += blockDim.x)
+                *reinterpret_cast<uint32_t*>(p.sf + sf_word(row, a, p.atoms_k)) = 0u;
+        return;
+    }
+    const int rows = static_cast<int>(min(static_cast<int64_t>(R), group_end - row0));
+    const size_t gbase = static_cast<size_t>(group) * p.K;
+    using Vec = Raw8<kVF32>;
+
+    // Channels past the end load the row's first ones instead and their values are zeroed.  Rows past
+    // the CTA's last load that one; they store nothing.
+    const uint32_t c0 = (threadIdx.x >> 5) * 256u + lane * 4u, step = blockDim.x * 8u;
+    bool live[C][2];
+    At at[C];
+    size_t base[R];
+    Raw8<kF32> z[R][C];  // x, then z
+    Raw8<false> y[R][C];
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+        const uint32_t c = c0 + j * step;
+        live[j][0] = kFull || c < p.K;
+        live[j][1] = kFull || c + 128u < p.K;
+        at[j].a = live[j][0] ? c : 0u;
+        at[j].b = live[j][1] ? c + 128u : 0u;
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        base[r] = static_cast<size_t>(row0 + min(r, rows - 1)) * p.K;
+#pragma unroll
+        for (int j = 0; j < C; ++j) z[r][j] = load_row8<kF32>(p.x, base[r], at[j]);
+    }
+    if (p.y) {
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int j = 0; j < C; ++j) y[r][j] = load_row8<false>(p.y, base[r], at[j]);
+    }
+    [[maybe_unused]] Vec w_r[C], b_r[C], s_r[C], t_r[C];
+    if constexpr (kEarly) {
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+            if (p.weight) w_r[j] = load_vec8<kVF32>(p.weight, 0, at[j]);
+            if (p.bias) b_r[j] = load_vec8<kVF32>(p.bias, 0, at[j]);
+            if (p.scale) s_r[j] = load_vec8<kVF32>(p.scale, gbase, at[j]);
+            if (p.shift) t_r[j] = load_vec8<kVF32>(p.shift, gbase, at[j]);
+        }
+    }
+
+    float neg_mean[R], rstd[R];
+    if (p.y) {
+        if (p.post != MXQ_NORM_NONE) {
+            if constexpr (!kFull) {
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int j = 0; j < C; ++j)
+                        zero_dead(y[r][j], live[j][0], live[j][1]);
+            }
+            row_stats<R, C, kFull>([&](int r, int j, float2(&t)[4]) { keep_packed(y[r][j]); widen8(y[r][j], t); }, live,
+                                   p.post, p.inv_k, p.eps, red + 2 * R * kMaxWarps, neg_mean, rstd);
+        }
+        // z = x + gate * u, chunk by chunk
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+            float2 u[R][1][4];
+            const At a1[1] = {at[j]};
+#pragma unroll
+            for (int r = 0; r < R; ++r) widen8(y[r][j], u[r][0]);
+            if (p.post != MXQ_NORM_NONE) {
+                normalize(u, neg_mean, rstd);
+                if (p.post_weight) apply_vec<kVF32>(u, p.post_weight, 0, a1, Mul());
+                if (p.post_bias) apply_vec<kVF32>(u, p.post_bias, 0, a1, Add());
+            }
+            if (p.gate) {
+                float2 t[4], xv[4];
+                widen8(load_vec8<kVF32>(p.gate, gbase, at[j]), t);
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    widen8(z[r][j], xv);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) u[r][0][i] = __ffma2_rn(t[i], u[r][0][i], xv[i]);
+                }
+            } else {
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    float2 xv[4];
+                    widen8(z[r][j], xv);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) u[r][0][i] = __fadd2_rn(u[r][0][i], xv[i]);
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                narrow8(u[r][0], z[r][j]);  // rounded to the stream's type; the norm sees this value
+                if (r < rows) store_row8(p.z, base[r], at[j], live[j][0], live[j][1], z[r][j]);
+            }
+        }
+    }
+    if constexpr (!kFull) {
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int j = 0; j < C; ++j)
+                zero_dead(z[r][j], live[j][0], live[j][1]);
+    }
+    row_stats<R, C, kFull>([&](int r, int j, float2(&t)[4]) { keep_packed(z[r][j]); widen8(z[r][j], t); }, live, p.norm,
+                           p.inv_k, p.eps, red, neg_mean, rstd);
+    float2 v[R][C][4];  // h
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+            keep_packed(z[r][j]);
+            widen8(z[r][j], v[r][j]);
+        }
+    normalize(v, neg_mean, rstd);
+    if constexpr (kEarly) {
+        if (p.weight) apply_vec<kVF32>(v, w_r, Mul());
+        if (p.bias) apply_vec<kVF32>(v, b_r, Add());
+        if (p.scale) apply_vec<kVF32>(v, s_r, MulOnePlus());
+        if (p.shift) apply_vec<kVF32>(v, t_r, Add());
+    } else {
+        if (p.weight) apply_vec<kVF32>(v, p.weight, 0, at, Mul());
+        if (p.bias) apply_vec<kVF32>(v, p.bias, 0, at, Add());
+        if (p.scale) apply_vec<kVF32>(v, p.scale, gbase, at, MulOnePlus());
+        if (p.shift) apply_vec<kVF32>(v, p.shift, gbase, at, Add());
+    }
+
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+            if (r < rows) emit<kQuant>(p, row0 + r, base[r], c0 + j * step, at[j], live[j][0], live[j][1], v[r][j]);
+        }
+}
+
+template <bool kF32, bool kVF32, bool kQuant, int C, int R, bool kFull, bool kEarly>
+cudaError_t launch_one(NormParams p, int warps, cudaStream_t stream)
+{
+    const int64_t groups = ceil_div(p.rows, p.rows_per_group);
+    p.row_blocks = groups * ceil_div(p.rows_per_group, R);
+    const int64_t grid = p.row_blocks + (kQuant ? p.rows_pad - p.rows : 0);
+    if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    norm_residual_kernel<kF32, kVF32, kQuant, C, R, kFull, kEarly><<<static_cast<unsigned>(grid), 32 * warps, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+// Few rows: a CTA each, as many warps as a row has spans (two spans a warp from 16 on), for the
+// shortest chain of loads.  Many rows: CTAs of at most ten warps (more wait longer at each
+// barrier) with one chunk a thread of four rows or two of two rows (of one, for a bf16 stream with
+// bf16 out); longer rows take two or four chunks a thread of one row.
+template <bool kF32, bool kVF32, bool kQuant>
+cudaError_t launch_shape(const NormParams& p, cudaStream_t stream)
+{
+    const int spans = static_cast<int>(ceil_div(p.K, 256));
+    const bool few = p.rows <= 2 * 148;
+    if (few && spans <= 32) {
+        if (spans <= 16) return launch_one<kF32, kVF32, kQuant, 1, 1, false, true>(p, spans, stream);
+        return launch_one<kF32, kVF32, kQuant, 2, 1, false, true>(p, static_cast<int>(ceil_div(spans, 2)), stream);
+    }
+    const int c = spans <= 10 ? 1 : spans <= 20 ? 2 : 4;
+    const int warps = static_cast<int>(ceil_div(spans, c));
+    const bool full = p.K % 256 == 0 && c * warps == spans;
+    if (c == 4)
+        return full ? launch_one<kF32, kVF32, kQuant, 4, 1, true, false>(p, warps, stream)
+                    : launch_one<kF32, kVF32, kQuant, 4, 1, false, false>(p, warps, stream);
+    if (c == 1)
+        return full ? launch_one<kF32, kVF32, kQuant, 1, 4, true, false>(p, warps, stream)
+                    : launch_one<kF32, kVF32, kQuant, 1, 4, false, false>(p, warps, stream);
+    constexpr int R = kF32 || kQuant ? 2 : 1;
+    if (spans > 20)
+        return full ? launch_one<kF32, kVF32, kQuant, 2, 1, true, false>(p, warps, stream)
+                    : launch_one<kF32, kVF32, kQuant, 2, 1, false, false>(p, warps, stream);
+    return full ? launch_one<kF32, kVF32, kQuant, 2, R, true, false>(p, warps, stream)
+                : launch_one<kF32, kVF32, kQuant, 2, R, false, false>(p, warps, stream);
 }
 
 }  // namespace
@@ -371,18 +615,15 @@ cudaError_t launch_norm_residual(const mxq_norm_desc& d, void* z, int out_fmt, v
     p.inv_k = static_cast<float>(1.0 / static_cast<double>(d.K));
     p.norm = d.norm;
     p.post = d.post_norm;
-    p.vec_f32 = d.vec_dtype == MXQ_DTYPE_F32;
-    // Few rows: as many threads as the row has chunks, for the shortest chain of loads.  Many
-    // rows: four chunks a thread, which keeps more bytes in flight per register.
-    const int chunks = p.K / 8;
-    const bool few = d.rows <= 2 * 148;
-    const int want = few ? chunks : std::max(64, static_cast<int>(ceil_div(chunks, 4)));
-    const int threads = std::min<int>(kMaxThreads, static_cast<int>(ceil_div(want, 32)) * 32);
-    const int c = static_cast<int>(ceil_div(chunks, threads));
-    const bool quant = out_fmt != MXQ_OUT_BF16;
-    const unsigned grid = static_cast<unsigned>(quant ? ceil_div(d.rows, 128) * 128 : d.rows);
-    return d.x_dtype == MXQ_DTYPE_F32 ? launch_out<true>(out_fmt, c, grid, threads, p, stream)
-                                      : launch_out<false>(out_fmt, c, grid, threads, p, stream);
+    p.rows_pad = ceil_div(d.rows, 128) * 128;
+    p.e4m3 = out_fmt == MXQ_FMT_E4M3;
+    const bool f = d.x_dtype == MXQ_DTYPE_F32, vf = d.vec_dtype == MXQ_DTYPE_F32;
+    if (out_fmt == MXQ_OUT_BF16) {
+        if (f) return vf ? launch_shape<true, true, false>(p, stream) : launch_shape<true, false, false>(p, stream);
+        return vf ? launch_shape<false, true, false>(p, stream) : launch_shape<false, false, false>(p, stream);
+    }
+    if (f) return vf ? launch_shape<true, true, true>(p, stream) : launch_shape<true, false, true>(p, stream);
+    return vf ? launch_shape<false, true, true>(p, stream) : launch_shape<false, false, true>(p, stream);
 }
 
 }  // namespace mxq

@@ -431,30 +431,41 @@ def _pick(table, key, what):
     return table[key]
 
 
-def _tensor(t, name, dtype, shape, device):
-    """t, checked to be a contiguous CUDA tensor of that dtype, shape and device."""
-    if not (t.is_cuda and t.dtype == dtype and t.is_contiguous() and t.shape == shape and t.device == device):
+def _tensor(t, name, dtype, shape, device) -> int:
+    """The address of t, checked to be a contiguous tensor of that dtype, shape and device."""
+    if not (t.dtype == dtype and t.shape == shape and t.is_contiguous() and t.device == device):
         raise ValueError("%s must be a contiguous %s tensor of shape %s on %s, got %s %s on %s" % (
             name, dtype, tuple(shape), device, t.dtype, tuple(t.shape), t.device))
-    return t
+    return t.data_ptr()
 
 
-def _on_current_device(x: torch.Tensor) -> None:
-    """The library launches on the current device: its tensors have to live there."""
-    if not x.is_cuda:
-        raise ValueError("expected CUDA tensors, got one on %s" % x.device)
-    if x.get_device() != torch.cuda.current_device():
-        raise ValueError("tensors are on %s but the current device is cuda:%d" % (x.device,
-                                                                                 torch.cuda.current_device()))
+def _opt(t, name, dtype, shape, device) -> int:
+    return 0 if t is None else _tensor(t, name, dtype, shape, device)
 
 
-def _group_vec(t, name, dtype, rows, K, rows_per_group, device):
-    """Pointer of per-group vectors [groups, K] ([K] for one group), or 0."""
+def _current_device(x: torch.Tensor) -> torch.device:
+    """x's device, which has to be the current one: the library launches there."""
+    dev = x.device
+    if dev.type != "cuda":
+        raise ValueError("expected CUDA tensors, got one on %s" % dev)
+    if dev.index != torch.cuda.current_device():
+        raise ValueError("tensors are on %s but the current device is cuda:%d" % (dev, torch.cuda.current_device()))
+    return dev
+
+
+def _raw_stream(stream, dev) -> int:
+    """The stream's handle: the given stream, or the device's current one."""
+    return torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
+
+
+def _group_vec(t, name, dtype, rows, K, rows_per_group, device) -> int:
+    """The address of per-group vectors [groups, K] ([K] for one group), or 0."""
     if t is None:
         return 0
     groups = -(-rows // rows_per_group)
-    ok = t.dim() == 2 and t.shape[0] >= groups or t.dim() == 1 and groups == 1
-    if not ok or t.shape[-1] != K or t.dtype != dtype or not t.is_contiguous() or t.device != device:
+    shape = t.shape
+    ok = len(shape) == 2 and shape[0] >= groups or len(shape) == 1 and groups == 1
+    if not ok or shape[-1] != K or t.dtype != dtype or not t.is_contiguous() or t.device != device:
         raise ValueError("%s must be a contiguous %s tensor [%d, %d] on %s, got %s %s on %s" % (
             name, dtype, groups, K, device, t.dtype, tuple(t.shape), t.device))
     return t.data_ptr()
@@ -468,6 +479,23 @@ def _rows_per_group(rows_per_group, rows):
     return int(rows_per_group)
 
 
+def _mx_bytes(rows: int, K: int, f: int):
+    """mxq_codes_bytes and mxq_sf_bytes, at least 1 (the library refuses sizes they do not fit)."""
+    return (max(1, rows * K if f == FMT_E4M3 else rows * K // 2),
+            max(1, (rows + 127) // 128 * 128 * ((K // 32 + 3) // 4) * 4))
+
+
+def _codes_out(codes, sf, rows, K, f, dev):
+    """The buffers of a quantized [rows, K] output: the caller's, checked, or new ones."""
+    nc, ns = _mx_bytes(rows, K, f)
+    for t, n, name in ((codes, nc, "codes"), (sf, ns, "sf")):
+        if t is not None and not (t.dtype == torch.uint8 and t.is_contiguous() and t.numel() >= n and t.device == dev):
+            raise ValueError("%s must be a contiguous uint8 tensor of at least %d bytes on %s" % (name, n, dev))
+    codes = torch.empty(nc, dtype=torch.uint8, device=dev) if codes is None else codes
+    sf = torch.empty(ns, dtype=torch.uint8, device=dev) if sf is None else sf
+    return codes, sf
+
+
 def norm_residual(x: torch.Tensor, y: torch.Tensor | None = None, norm="layer", weight=None, bias=None, gate=None,
                   scale=None, shift=None, rows_per_group=None, post_norm="none", post_weight=None, post_bias=None,
                   eps=1e-6, out_fmt="bf16", z=None, h=None, codes=None, sf=None, stream=None):
@@ -479,51 +507,49 @@ def norm_residual(x: torch.Tensor, y: torch.Tensor | None = None, norm="layer", 
     [K] are all bf16 or all float32; row r uses group r // rows_per_group.  Returns (z, h)
     with h bf16, or, for out_fmt "e2m1" / "e4m3", (z, codes, tiled scales): the bits that
     quantize_act writes for that h.  z may be x; no other output may overlap an input."""
-    _on_current_device(x)
-    if x.dim() != 2 or x.dtype not in _VEC_DTYPES or not x.is_contiguous():
+    dev = _current_device(x)
+    xdt = x.dtype
+    if xdt not in _VEC_DTYPES or x.dim() != 2 or not x.is_contiguous():
         raise ValueError("x must be a contiguous bf16 or float32 tensor [rows, K]")
-    rows, K = x.shape
-    dev = x.device
+    shape = x.shape
+    rows, K = shape
     f = _pick(_OUTS, out_fmt, "out_fmt")
     rpg = _rows_per_group(rows_per_group, rows)
-    vdt = next((v.dtype for v in (weight, bias, post_weight, post_bias, gate, scale, shift) if v is not None),
-               torch.float32)
+    vdt = torch.float32  # of the channel vectors, unless one of them says otherwise
+    for v in (weight, bias, post_weight, post_bias, gate, scale, shift):
+        if v is not None:
+            vdt = v.dtype
+            break
     if vdt not in _VEC_DTYPES:
         raise ValueError("the channel vectors must be bf16 or float32, got %s" % vdt)
-    w, b, pw, pb = (0 if v is None else _tensor(v, n, vdt, (K,), dev).data_ptr()
-                    for v, n in ((weight, "weight"), (bias, "bias"), (post_weight, "post_weight"),
-                                 (post_bias, "post_bias")))
-    g, sc, sh = (_group_vec(v, n, vdt, rows, K, rpg, dev)
-                 for v, n in ((gate, "gate"), (scale, "scale"), (shift, "shift")))
+    zp = 0
     if y is not None:
-        _tensor(y, "y", torch.bfloat16, x.shape, dev)
-        z = torch.empty_like(x) if z is None else _tensor(z, "z", x.dtype, x.shape, dev)
+        if z is None:
+            z = torch.empty_like(x)
+            zp = z.data_ptr()
+        else:
+            zp = _tensor(z, "z", xdt, shape, dev)
     elif z is not None:
         raise ValueError("z goes with y")
     if f == _lib.OUT_BF16:
-        out = torch.empty((rows, K), dtype=torch.bfloat16, device=dev) if h is None else _tensor(
-            h, "h", torch.bfloat16, x.shape, dev)
+        out = _bf16_out(h, rows, K, dev, "h")
     else:
         out, sf = _codes_out(codes, sf, rows, K, f, dev)
-    d = _lib.NormDesc(x.data_ptr(), 0 if y is None else y.data_ptr(), rows, K, _VEC_DTYPES[x.dtype],
-                      _VEC_DTYPES[vdt], _pick(_NORMS, norm, "norm"), _pick(_NORMS, post_norm, "post_norm"), w, b, pw,
-                      pb, g, sc, sh, rpg, eps)
-    check(_lib.lib().mxq_norm_residual(d, _p(z), f, _p(out), _p(None if f == _lib.OUT_BF16 else sf),
-                                       _stream(stream)), "mxq_norm_residual")
+    d = _lib.NormDesc(x.data_ptr(), _opt(y, "y", torch.bfloat16, shape, dev), rows, K, _VEC_DTYPES[xdt],
+                      _VEC_DTYPES[vdt], _pick(_NORMS, norm, "norm"), _pick(_NORMS, post_norm, "post_norm"),
+                      _opt(weight, "weight", vdt, (K,), dev), _opt(bias, "bias", vdt, (K,), dev),
+                      _opt(post_weight, "post_weight", vdt, (K,), dev), _opt(post_bias, "post_bias", vdt, (K,), dev),
+                      _group_vec(gate, "gate", vdt, rows, K, rpg, dev),
+                      _group_vec(scale, "scale", vdt, rows, K, rpg, dev),
+                      _group_vec(shift, "shift", vdt, rows, K, rpg, dev), rpg, eps)
+    quant = f != _lib.OUT_BF16
+    check(_lib.lib().mxq_norm_residual(d, zp, f, out.data_ptr(), sf.data_ptr() if quant else 0,
+                                       _raw_stream(stream, dev)), "mxq_norm_residual")
     z = x if y is None else z
-    return (z, out) if f == _lib.OUT_BF16 else (z, out, sf)
+    return (z, out, sf) if quant else (z, out)
 
 
-def _codes_out(codes, sf, rows, K, f, dev):
-    """The buffers of a quantized [rows, K] output: the caller's, checked, or new ones."""
-    nc, ns = max(1, codes_bytes(rows, K, f)), max(1, sf_bytes(rows, K))
-    for t, n, name in ((codes, nc, "codes"), (sf, ns, "sf")):
-        if t is not None and not (t.dtype == torch.uint8 and t.is_contiguous() and t.numel() >= n and t.device == dev):
-            raise ValueError("%s must be a contiguous uint8 tensor of at least %d bytes on %s" % (name, n, dev))
-    codes = torch.empty(nc, dtype=torch.uint8, device=dev) if codes is None else codes
-    sf = torch.empty(ns, dtype=torch.uint8, device=dev) if sf is None else sf
-    return codes, sf
-
+ROWS_QUANTIZED_IN_KERNEL = 16  # mxq_linear_residual quantizes so few rows inside its GEMM kernel
 
 _ACTS = {"none": _lib.ACT_NONE, "gelu": _lib.ACT_GELU, "gelu_tanh": _lib.ACT_GELU_TANH, "silu": _lib.ACT_SILU}
 
@@ -535,37 +561,38 @@ def _act(a) -> int:
 def _epilogue(act, residual, gate, rows_per_group, M, N, dev):
     """The checked mxq_epilogue of an [M, N] output."""
     rpg = _rows_per_group(rows_per_group, M)
-    if residual is not None:
-        _tensor(residual, "residual", torch.bfloat16, (M, N), dev)
     gdt = torch.bfloat16 if gate is None else gate.dtype
     if gdt not in _VEC_DTYPES:
         raise ValueError("gate must be bf16 or float32, got %s" % gdt)
-    return _lib.Epilogue(_act(act), _VEC_DTYPES[gdt], 0 if residual is None else residual.data_ptr(),
+    return _lib.Epilogue(_act(act), _VEC_DTYPES[gdt], _opt(residual, "residual", torch.bfloat16, (M, N), dev),
                          _group_vec(gate, "gate", gdt, M, N, rpg, dev), rpg)
 
 
-def _check_operand(codes, sf, M, K, f):
+def _operand(codes, sf, M, K, f) -> torch.device:
     """The device of a quantized [M, K] operand, its buffers checked."""
-    _on_current_device(codes)
-    for t, n, name in ((codes, codes_bytes(M, K, f), "a_codes"), (sf, sf_bytes(M, K), "a_sf")):
-        if not t.is_contiguous() or t.numel() * t.element_size() < n or t.device != codes.device:
-            raise ValueError("%s must be a contiguous tensor of at least %d bytes on %s" % (name, n, codes.device))
-    return codes.device
+    dev = _current_device(codes)
+    nc, ns = _mx_bytes(M, K, f)
+    if not (codes.nbytes >= nc and sf.nbytes >= ns and codes.is_contiguous() and sf.is_contiguous() and
+            sf.device == dev):
+        raise ValueError("a_codes and a_sf must be contiguous tensors of %d and %d bytes on %s" % (nc, ns, dev))
+    return dev
 
 
-def _check_qweight(w: QWeight, name, dev):
-    if w.codes.device != dev or w.sf.device != dev or w.bias is not None and w.bias.device != dev:
-        raise ValueError("%s must be on %s" % (name, dev))
-    if w.bias is not None:
-        _tensor(w.bias, name + ".bias", torch.bfloat16, (w.N,), dev)
+def _qweight(w: QWeight, name, dev) -> WDesc:
+    """The checked descriptor of a weight."""
+    N, K, codes, sf, bias = w.N, w.K, w.codes, w.sf, w.bias
+    nc, ns = _mx_bytes(N, K, FMT_E2M1)
+    if not (codes.nbytes >= nc and sf.nbytes >= ns and codes.is_contiguous() and sf.is_contiguous() and
+            codes.device == dev and sf.device == dev):
+        raise ValueError("%s must hold contiguous tensors of %d and %d bytes on %s" % (name, nc, ns, dev))
+    return WDesc(codes.data_ptr(), sf.data_ptr(), _opt(bias, "bias", torch.bfloat16, (N,), dev), N, K)
 
 
-def _check_x(x):
-    _on_current_device(x)
-    _cuda_bf16(x, "x")
-    if x.dim() != 2:
-        raise ValueError("x must be [M, K], got %s" % (tuple(x.shape),))
-    return x.device
+def _bf16_x(x, name) -> torch.device:
+    dev = _current_device(x)
+    if x.dtype != torch.bfloat16 or x.dim() != 2 or not x.is_contiguous():
+        raise ValueError("%s must be a contiguous bf16 tensor [rows, K], got %s %s" % (name, x.dtype, tuple(x.shape)))
+    return dev
 
 
 def _workspace(ws, need, dev):
@@ -576,9 +603,16 @@ def _workspace(ws, need, dev):
     return ws
 
 
-def _bf16_out(out, M, N, dev):
-    return torch.empty((M, N), dtype=torch.bfloat16, device=dev) if out is None else _tensor(
-        out, "out", torch.bfloat16, (M, N), dev)
+def _bf16_out(out, M, N, dev, name="out"):
+    if out is None:
+        return torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+    _tensor(out, name, torch.bfloat16, (M, N), dev)
+    return out
+
+
+def _check_k(w: QWeight, K, name="w"):
+    if w.K != K:
+        raise ValueError("%s has K=%d but the activation has %d" % (name, w.K, K))
 
 
 def gemm_residual(a_codes, a_sf, fmt, M: int, K: int, w: QWeight, act="none", residual=None, gate=None,
@@ -588,12 +622,13 @@ def gemm_residual(a_codes, a_sf, fmt, M: int, K: int, w: QWeight, act="none", re
     bf16 (it may be out); gate [groups, N] or [N], bf16 or float32, row m using group
     m // rows_per_group (default: one group)."""
     f = _fmt(fmt)
-    dev = _check_operand(a_codes, a_sf, M, K, f)
-    _check_qweight(w, "w", dev)
+    dev = _operand(a_codes, a_sf, M, K, f)
+    _check_k(w, K)
+    d = _qweight(w, "w", dev)
     e = _epilogue(act, residual, gate, rows_per_group, M, w.N, dev)
     out = _bf16_out(out, M, w.N, dev)
-    check(_lib.lib().mxq_gemm_residual(_p(a_codes), _p(a_sf), f, M, K, _p(w.codes), _p(w.sf), w.N, _p(w.bias), e,
-                                       _p(out), _stream(stream)), "mxq_gemm_residual")
+    check(_lib.lib().mxq_gemm_residual(a_codes.data_ptr(), a_sf.data_ptr(), f, M, K, d.codes, d.sf, w.N, d.bias, e,
+                                       out.data_ptr(), _raw_stream(stream, dev)), "mxq_gemm_residual")
     return out
 
 
@@ -601,38 +636,41 @@ def gemm_bf16_residual(a: torch.Tensor, b: torch.Tensor, bias: torch.Tensor | No
                        gate=None, rows_per_group=None, out=None, stream=None):
     """y = residual + gate * act(a . b^T + bias) in bf16 with fp32 accumulation, a [M, K] and
     b [N, K] bf16; the other arguments as for gemm_residual."""
-    dev = _check_x(a)
+    dev = _bf16_x(a, "a")
     M, K = a.shape
     N = b.shape[0]
-    _tensor(b, "b", torch.bfloat16, (N, K), dev)
-    if bias is not None:
-        _tensor(bias, "bias", torch.bfloat16, (N,), dev)
+    bp = _tensor(b, "b", torch.bfloat16, (N, K), dev)
     e = _epilogue(act, residual, gate, rows_per_group, M, N, dev)
     out = _bf16_out(out, M, N, dev)
-    check(_lib.lib().mxq_gemm_bf16_residual(_p(a), M, K, _p(b), N, _p(bias), e, _p(out), _stream(stream)),
-          "mxq_gemm_bf16_residual")
+    check(_lib.lib().mxq_gemm_bf16_residual(a.data_ptr(), M, K, bp, N, _opt(bias, "bias", torch.bfloat16, (N,), dev),
+                                            e, out.data_ptr(), _raw_stream(stream, dev)), "mxq_gemm_bf16_residual")
     return out
 
 
 def linear_residual(x: torch.Tensor, w: QWeight, fmt="e2m1", act="none", residual=None, gate=None,
                     rows_per_group=None, workspace=None, out=None, stream=None):
     """linear() with gemm_residual's epilogue: x quantized on the fly to fmt, then
-    y = residual + gate * act(x . deq(w)^T + bias)."""
-    dev = _check_x(x)
+    y = residual + gate * act(x . deq(w)^T + bias).  workspace of
+    workspace_bytes(M, N, K, fmt) bytes; up to ROWS_QUANTIZED_IN_KERNEL rows need none."""
+    dev = _bf16_x(x, "x")
     M, K = x.shape
     f = _fmt(fmt)
-    _check_qweight(w, "w", dev)
+    _check_k(w, K)
+    d = _qweight(w, "w", dev)
     e = _epilogue(act, residual, gate, rows_per_group, M, w.N, dev)
-    workspace = _workspace(workspace, workspace_bytes(M, w.N, K, f, MODE_NATIVE), dev)
+    ws = wsb = 0
+    if workspace is not None or M > ROWS_QUANTIZED_IN_KERNEL:
+        nc, ns = _mx_bytes(M, K, f)
+        workspace = _workspace(workspace, (nc + 255) // 256 * 256 + (ns + 255) // 256 * 256, dev)
+        ws, wsb = workspace.data_ptr(), workspace.nbytes
     out = _bf16_out(out, M, w.N, dev)
-    check(_lib.lib().mxq_linear_residual(_p(x), M, K, _p(w.codes), _p(w.sf), w.N, _p(w.bias), f, e, _p(workspace),
-                                         workspace.numel() * workspace.element_size(), _p(out), _stream(stream)),
-          "mxq_linear_residual")
+    check(_lib.lib().mxq_linear_residual(x.data_ptr(), M, K, d.codes, d.sf, w.N, d.bias, f, e, ws, wsb,
+                                         out.data_ptr(), _raw_stream(stream, dev)), "mxq_linear_residual")
     return out
 
 
 def _gated_out(M, H, out_fmt, out, codes, sf, dev):
-    """(out_fmt, h or codes, scales) of a gated GEMM."""
+    """(out_fmt, h or codes, scales or None) of a gated GEMM."""
     f = _pick(_OUTS, out_fmt, "out_fmt")
     if f == _lib.OUT_BF16:
         return f, _bf16_out(out, M, H, dev), None
@@ -646,29 +684,26 @@ def gemm_gated(a_codes, a_sf, fmt, M: int, K: int, gate: QWeight, up: QWeight, a
     on an already-quantized activation.  Returns h in bf16, or, for out_fmt "e2m1" / "e4m3",
     (codes, tiled scales): the bits that quantize_act writes for that h."""
     f = _fmt(fmt)
-    dev = _check_operand(a_codes, a_sf, M, K, f)
-    _check_qweight(gate, "gate", dev)
-    _check_qweight(up, "up", dev)
+    dev = _operand(a_codes, a_sf, M, K, f)
+    dg, du = _qweight(gate, "gate", dev), _qweight(up, "up", dev)
     of, o, so = _gated_out(M, gate.N, out_fmt, out, codes, sf, dev)
-    check(_lib.lib().mxq_gemm_gated(_p(a_codes), _p(a_sf), f, M, K, gate.desc(), up.desc(), _act(act), of, _p(o),
-                                    _p(so), _stream(stream)), "mxq_gemm_gated")
+    check(_lib.lib().mxq_gemm_gated(a_codes.data_ptr(), a_sf.data_ptr(), f, M, K, dg, du, _act(act), of, o.data_ptr(),
+                                    0 if so is None else so.data_ptr(), _raw_stream(stream, dev)), "mxq_gemm_gated")
     return o if so is None else (o, so)
 
 
 def gemm_bf16_gated(a: torch.Tensor, gate: torch.Tensor, up: torch.Tensor, gate_bias=None, up_bias=None, act="silu",
                     out_fmt="bf16", out=None, codes=None, sf=None, stream=None):
     """gemm_gated on bf16 operands: a [M, K], gate and up [H, K]."""
-    dev = _check_x(a)
+    dev = _bf16_x(a, "a")
     M, K = a.shape
     H = gate.shape[0]
-    for t, name in ((gate, "gate"), (up, "up")):
-        _tensor(t, name, torch.bfloat16, (H, K), dev)
-    for t, name in ((gate_bias, "gate_bias"), (up_bias, "up_bias")):
-        if t is not None:
-            _tensor(t, name, torch.bfloat16, (H,), dev)
+    gp, up_ = _tensor(gate, "gate", torch.bfloat16, (H, K), dev), _tensor(up, "up", torch.bfloat16, (H, K), dev)
+    gb, ub = (_opt(b, n, torch.bfloat16, (H,), dev) for b, n in ((gate_bias, "gate_bias"), (up_bias, "up_bias")))
     of, o, so = _gated_out(M, H, out_fmt, out, codes, sf, dev)
-    check(_lib.lib().mxq_gemm_bf16_gated(_p(a), M, K, _p(gate), _p(gate_bias), _p(up), _p(up_bias), H, _act(act), of,
-                                         _p(o), _p(so), _stream(stream)), "mxq_gemm_bf16_gated")
+    check(_lib.lib().mxq_gemm_bf16_gated(a.data_ptr(), M, K, gp, gb, up_, ub, H, _act(act), of, o.data_ptr(),
+                                         0 if so is None else so.data_ptr(), _raw_stream(stream, dev)),
+          "mxq_gemm_bf16_gated")
     return o if so is None else (o, so)
 
 
@@ -680,17 +715,17 @@ def gated_ffn(x: torch.Tensor, gate: QWeight, up: QWeight, down: QWeight, act="s
     activation kept quantized in down_fmt.  residual, out_gate and rows_per_group as
     gemm_residual's residual, gate and rows_per_group; workspace of
     ffn_workspace_bytes(M, K, H, up_fmt, down_fmt) bytes."""
-    dev = _check_x(x)
+    dev = _bf16_x(x, "x")
     M, K = x.shape
-    for w, name in ((gate, "gate"), (up, "up"), (down, "down")):
-        _check_qweight(w, name, dev)
+    dg, du, dd = _qweight(gate, "gate", dev), _qweight(up, "up", dev), _qweight(down, "down", dev)
     e = _epilogue("none", residual, out_gate, rows_per_group, M, down.N, dev)
     uf, df = _fmt(up_fmt), _fmt(down_fmt)
-    workspace = _workspace(workspace, ffn_workspace_bytes(M, K, gate.N, uf, df), dev)
+    need = sum((n + 255) // 256 * 256 for n in _mx_bytes(M, K, uf) + _mx_bytes(M, gate.N, df))
+    workspace = _workspace(workspace, need, dev)
     out = _bf16_out(out, M, down.N, dev)
-    check(_lib.lib().mxq_gated_ffn(_p(x), M, K, gate.desc(), up.desc(), down.desc(), _act(act), uf, df, e,
-                                   _p(workspace), workspace.numel() * workspace.element_size(), _p(out),
-                                   _stream(stream)), "mxq_gated_ffn")
+    check(_lib.lib().mxq_gated_ffn(x.data_ptr(), M, K, dg, du, dd, _act(act), uf, df, e, workspace.data_ptr(),
+                                   workspace.nbytes, out.data_ptr(),
+                                   _raw_stream(stream, dev)), "mxq_gated_ffn")
     return out
 
 

@@ -467,7 +467,9 @@ int mxq_gemm_bf16_residual(const void* a_bf16, int64_t M, int64_t K, const void*
                            const void* bias_bf16, const mxq_epilogue* e, void* y_bf16, void* stream);
 
 /* mxq_linear (mode NATIVE) with that epilogue: x quantized to act_fmt into the workspace of
- * mxq_workspace_bytes(M, N, K, act_fmt, MXQ_MODE_NATIVE) bytes, then mxq_gemm_residual. */
+ * mxq_workspace_bytes(M, N, K, act_fmt, MXQ_MODE_NATIVE) bytes, then mxq_gemm_residual.  Up to
+ * 16 rows are quantized inside the GEMM kernel, to the same codes; workspace is then not used
+ * and may be NULL. */
 int mxq_linear_residual(const void* x_bf16, int64_t M, int64_t K, const void* w_codes, const void* w_sf, int64_t N,
                         const void* bias_bf16, int act_fmt, const mxq_epilogue* e, void* workspace, int64_t ws_bytes,
                         void* y_bf16, void* stream);
