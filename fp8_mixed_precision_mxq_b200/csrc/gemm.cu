@@ -133,9 +133,14 @@ constexpr int kOutGatedE4M3 = 8;
 template <int kOut>
 constexpr bool kOutE4M3 = kOut == kOutGeluE4M3 || kOut == kOutQE4M3 || kOut == kOutGatedE4M3;
 template <int kOut>  // bf16 staging buffers (y, or h on request)
-constexpr bool kOutEbuf = kOut <= kOutGeluE4M3 || kOut == kOutRes || kOut == kOutGated;
+constexpr bool kOutEbuf = kOut <= kOutGeluE4M3;
 template <int kOut>  // the next layer's MX operand is written
 constexpr bool kOutQuant = (kOut >= kOutGeluE2M1 && kOut <= kOutQE4M3) || kOut >= kOutGatedE2M1;
+// The residual and gated epilogues store from their registers, 32 bytes a lane: a whole sector,
+// which TMA stores of 64-byte rows behind the mainloop's loads, and 16-byte stores, do not
+// match (32760 x 5120 x 5120 W4A4 with residual and gate: 448 us, against 586 and 534).
+template <int kOut>
+constexpr bool kOutDirect = kOut >= kOutRes;
 template <int kOut>  // GELU from the table
 constexpr bool kOutLut = kOut >= kOutGeluE2M1 && kOut <= kOutQE4M3;
 template <int kOut>
@@ -167,13 +172,8 @@ struct Cfg {
     // otherwise leave no room for the GELU table
     static constexpr int kQBufs = kOutE4M3<kOut> ? 1 : 2;
     static constexpr int kEpiWarps = kEpiWarpsOf<kOut>;
-    // bf16 staging buffers per warp: two, or one for the eight-warp epilogues that write
-    // nothing else (a chunk's store has long been read when the warp's next chunk is ready),
-    // which keeps the sixth pipeline stage
-    static constexpr int kEbufs = kOut >= kOutRes ? 1 : 2;
-    static constexpr bool kOneBuf = kOutE4M3<kOut> || (kEbufs == 1 && kOutEbuf<kOut>);  // staging not doubled
-    static constexpr uint32_t kOffQ = kOffEpi + (kOutEbuf<kOut> ? kEpiWarps * kEbufs * kEpiBuf : 0u);
-    static constexpr uint32_t kOffLut = kOffQ + (kOutQuant<kOut> ? kEpiWarps * kQBufs * kQBuf : 0u);  // GELU table
+    static constexpr uint32_t kOffQ = kOffEpi + (kOutEbuf<kOut> ? kEpiWarps * 2 * kEpiBuf : 0u);
+    static constexpr uint32_t kOffLut = kOffQ + (kOutLut<kOut> ? kEpiWarps * kQBufs * kQBuf : 0u);  // GELU table
     static constexpr uint32_t kOffBar = kOffLut + (kOutLut<kOut> ? kGeluTableBytes : 0u);
     static constexpr uint32_t kNumBars = 2 * kStages + 6 + 2 * kSfBufs;
     static constexpr uint32_t kSmemBytes = kOffBar + kNumBars * 8 + 16;
@@ -209,6 +209,9 @@ struct Params {
     // the latter the second projection's bias
     int act;
     int gate_f32;
+    __nv_bfloat16* y;  // their output (q_sf its scales), written from registers
+    uint8_t* q_codes;
+    int wide;          // its rows, and res's, are 32-byte aligned
     const __nv_bfloat16* res;
     const void* gate;
     uint32_t rows_per_group;
@@ -228,6 +231,61 @@ __device__ __forceinline__ void load_gate8(const void* gate, int f32, size_t i, 
         const uint4 a = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(gate) + i));
         v[0] = lo_f(a.x); v[1] = hi_f(a.x); v[2] = lo_f(a.y); v[3] = hi_f(a.y);
         v[4] = lo_f(a.z); v[5] = hi_f(a.z); v[6] = lo_f(a.w); v[7] = hi_f(a.w);
+    }
+}
+
+// One MX block of the next layer's operand from its 32 bf16 values (pairs in o): the E8M0 scale,
+// returned, and the element codes, rounded to nearest even by cvt; a non-finite block gets scale
+// 255 and codes 0.
+template <bool kE4M3>
+__device__ __forceinline__ uint32_t quantize_block(const uint32_t (&o)[16], uint32_t (&cw)[kE4M3 ? 8 : 4])
+{
+    uint32_t m2 = o[0];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) m2 = absmax_bf16x2(m2, o[i]);
+    m2 = absmax_bf16x2(m2, __byte_perm(m2, 0, 0x1032));
+    const uint32_t sc = e8m0_code<kE4M3 ? 8u : 2u>(m2);
+    const float inv = e8m0_inverse(sc);
+    const uint32_t keep = sc == 255u ? 0u : 0xFFFFFFFFu;
+    const float2 inv2 = make_float2(inv, inv);
+    if constexpr (!kE4M3) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = __fmul2_rn(make_float2(lo_f(o[4 * k + i]), hi_f(o[4 * k + i])), inv2);
+                v[2 * i] = f.x;
+                v[2 * i + 1] = f.y;
+            }
+            cw[k] = cvt_e2m1x8(v) & keep;
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float2 f0 = __fmul2_rn(make_float2(lo_f(o[2 * k]), hi_f(o[2 * k])), inv2);
+            const float2 f1 = __fmul2_rn(make_float2(lo_f(o[2 * k + 1]), hi_f(o[2 * k + 1])), inv2);
+            cw[k] = (cvt_e4m3x2(f0.x, f0.y) | (cvt_e4m3x2(f1.x, f1.y) << 16)) & keep;
+        }
+    }
+    return sc;
+}
+
+// A lane's 32 bf16 columns (pairs in o) of its output row, from column n of N on (both multiples
+// of 8), by 32-byte stores where the rows allow.
+__device__ __forceinline__ void store_columns(__nv_bfloat16* to, const uint32_t (&o)[16], int n, int N, bool wide)
+{
+    if (wide) {
+#pragma unroll
+        for (int g = 0; g < 4; g += 2)
+            if (n + 8 * g < N)
+                st_global_v8(to + 8 * g, make_uint4(o[4 * g], o[4 * g + 1], o[4 * g + 2], o[4 * g + 3]),
+                             make_uint4(o[4 * g + 4], o[4 * g + 5], o[4 * g + 6], o[4 * g + 7]));
+    } else {
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+            if (n + 8 * g < N)
+                reinterpret_cast<uint4*>(to)[g] = make_uint4(o[4 * g], o[4 * g + 1], o[4 * g + 2], o[4 * g + 3]);
     }
 }
 
@@ -301,8 +359,8 @@ __global__ void __launch_bounds__(kThreadsFor<kOut, kQA>, 1)
         prefetch_tmap(&map_b);
         prefetch_tmap(&map_sfa);
         prefetch_tmap(&map_sfb);
-        if (kOut == kOutBf16 || kOut >= kOutRes || (kOutEbuf<kOut> && p.write_h)) prefetch_tmap(&map_y);
-        if (kOutQuant<kOut>) prefetch_tmap(&map_q);
+        if (kOut == kOutBf16 || (kOutEbuf<kOut> && p.write_h)) prefetch_tmap(&map_y);
+        if (kOutLut<kOut>) prefetch_tmap(&map_q);
         if (p.lr_stages > 0 || kOutIsGated<kOut>) {
             prefetch_tmap(&map_u);
             prefetch_tmap(&map_l2);
@@ -641,7 +699,7 @@ __global__ void __launch_bounds__(kThreadsFor<kOut, kQA>, 1)
         const int ew = warp - 2;
         const int q = warp & 3;  // TMEM lane quarter this warp may access
         const uint32_t lanes = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
-        uint8_t* ebuf0 = smem + C::kOffEpi + ew * C::kEbufs * kEpiBuf;
+        uint8_t* ebuf0 = smem + C::kOffEpi + ew * 2 * kEpiBuf;
         uint8_t* qbuf0 = smem + C::kOffQ + ew * C::kQBufs * C::kQBuf;
         const uint16_t* lut = reinterpret_cast<const uint16_t*>(smem + C::kOffLut);
         if constexpr (kOutLut<kOut>) {
@@ -680,10 +738,17 @@ __global__ void __launch_bounds__(kThreadsFor<kOut, kQA>, 1)
             [[maybe_unused]] auto load_res = [&](int c) __attribute__((always_inline)) {
                 const int n = nb * BN + c * 32;
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    res4[g] = make_uint4(0u, 0u, 0u, 0u);
-                    if (p.res != nullptr && res_row < p.M && n + 8 * g < p.N)
-                        res4[g] = __ldcs(reinterpret_cast<const uint4*>(p.res + static_cast<size_t>(res_row) * p.N + n) + g);
+                for (int g = 0; g < 4; ++g) res4[g] = make_uint4(0u, 0u, 0u, 0u);
+                if (p.res == nullptr || res_row >= p.M) return;
+                const __nv_bfloat16* from = p.res + static_cast<size_t>(res_row) * p.N + n;
+                if (p.wide) {
+#pragma unroll
+                    for (int g = 0; g < 4; g += 2)
+                        if (n + 8 * g < p.N) ld_global_v8(from + 8 * g, res4[g], res4[g + 1]);
+                } else {
+#pragma unroll
+                    for (int g = 0; g < 4; ++g)
+                        if (n + 8 * g < p.N) res4[g] = __ldcs(reinterpret_cast<const uint4*>(from) + g);
                 }
             };
             if constexpr (kOut == kOutRes) {
@@ -726,11 +791,11 @@ __global__ void __launch_bounds__(kThreadsFor<kOut, kQA>, 1)
             // block's scale byte
             auto emit = [&](const uint32_t(&o)[16], int n) __attribute__((always_inline)) -> uint32_t {
                 uint32_t sc_byte = 0u;
-                                    const bool store_y = kOut == kOutBf16 || kOut >= kOutRes || (kOutEbuf<kOut> && p.write_h);
-                                    uint8_t* buf = ebuf0 + (C::kEbufs == 2 ? eb : 0) * kEpiBuf;
+                                    const bool store_y = kOut == kOutBf16 || (kOutEbuf<kOut> && p.write_h);
+                                    uint8_t* buf = ebuf0 + eb * kEpiBuf;
                                     // the stores that last used this chunk's buffers have read them
                                     if (lane == 0) {
-                                        if constexpr (C::kOneBuf)
+                                        if constexpr (C::kQBufs == 1)
                                             bulk_wait_read<0>();
                                         else
                                             bulk_wait_read<1>();
@@ -745,45 +810,14 @@ __global__ void __launch_bounds__(kThreadsFor<kOut, kQA>, 1)
                                         }
                                     }
                                     if constexpr (kOutQuant<kOut>) {
-                                        // this lane's 32 values are one MX block of the next layer's K: its
-                                        // E8M0 scale and element codes, rounded to nearest even by cvt
-                                        constexpr uint32_t kEmax = kOutE4M3<kOut> ? 8u : 2u;
-                                        uint32_t m2 = o[0];
-                #pragma unroll
-                                        for (int i = 1; i < 16; ++i) m2 = absmax_bf16x2(m2, o[i]);
-                                        m2 = absmax_bf16x2(m2, __byte_perm(m2, 0, 0x1032));
-                                        const uint32_t sc = e8m0_code<kEmax>(m2);
-                                        const float inv = e8m0_inverse(sc);
-                                        const uint32_t keep = sc == 255u ? 0u : 0xFFFFFFFFu;  // a non-finite block: codes 0
-                                        uint8_t* qb = qbuf0 + (C::kQBufs == 2 ? eb : 0) * C::kQBuf;
-                                        if constexpr (!kOutE4M3<kOut>) {
-                                            uint32_t cw[4];
-                                            const float2 inv2 = make_float2(inv, inv);
-                #pragma unroll
-                                            for (int k = 0; k < 4; ++k) {
-                                                float v[8];
-                #pragma unroll
-                                                for (int i = 0; i < 4; ++i) {
-                                                    const float2 f = __fmul2_rn(make_float2(lo_f(o[4 * k + i]), hi_f(o[4 * k + i])), inv2);
-                                                    v[2 * i] = f.x;
-                                                    v[2 * i + 1] = f.y;
-                                                }
-                                                cw[k] = cvt_e2m1x8(v) & keep;
-                                            }
-                                            *reinterpret_cast<uint4*>(qb + lane * 16) = make_uint4(cw[0], cw[1], cw[2], cw[3]);
-                                        } else {
-                                            uint32_t cw[8];
-                                            const float2 inv2 = make_float2(inv, inv);
-                #pragma unroll
-                                            for (int k = 0; k < 8; ++k) {
-                                                const float2 f0 = __fmul2_rn(make_float2(lo_f(o[2 * k]), hi_f(o[2 * k])), inv2);
-                                                const float2 f1 = __fmul2_rn(make_float2(lo_f(o[2 * k + 1]), hi_f(o[2 * k + 1])), inv2);
-                                                cw[k] = (cvt_e4m3x2(f0.x, f0.y) | (cvt_e4m3x2(f1.x, f1.y) << 16)) & keep;
-                                            }
-                                            *reinterpret_cast<uint4*>(qb + lane * 32) = make_uint4(cw[0], cw[1], cw[2], cw[3]);
-                                            *reinterpret_cast<uint4*>(qb + lane * 32 + 16) = make_uint4(cw[4], cw[5], cw[6], cw[7]);
-                                        }
-                                        sc_byte = sc;
+                                        // this lane's 32 values are one MX block of the next layer's K
+                    uint8_t* qb = qbuf0 + (C::kQBufs == 2 ? eb : 0) * C::kQBuf;
+                    uint32_t cw[kOutE4M3<kOut> ? 8 : 4];
+                    sc_byte = quantize_block<kOutE4M3<kOut>>(o, cw);
+#pragma unroll
+                    for (int k = 0; k < (kOutE4M3<kOut> ? 2 : 1); ++k)
+                        *reinterpret_cast<uint4*>(qb + lane * (kOutE4M3<kOut> ? 32 : 16) + 16 * k) =
+                            make_uint4(cw[4 * k], cw[4 * k + 1], cw[4 * k + 2], cw[4 * k + 3]);
                                     }
                                     fence_async_smem();
                                     __syncwarp();
@@ -848,7 +882,7 @@ __global__ void __launch_bounds__(kThreadsFor<kOut, kQA>, 1)
                         }
                     }
                 });
-                emit(o, n);
+                if (res_row < p.M) store_columns(p.y + static_cast<size_t>(res_row) * p.N + n, o, n, p.N, p.wide);
             };
             [[maybe_unused]] auto process = [&](const uint32_t(&acc)[32], int ci) __attribute__((always_inline)) {
                 const int c = chunk_of(ci);
@@ -945,7 +979,29 @@ __global__ void __launch_bounds__(kThreadsFor<kOut, kQA>, 1)
                                 }
                             }
                         });
-                        sc_byte = emit(o, n);
+                        const int row = row0 + lane;
+                        if constexpr (!kOutQuant<kOut>) {
+                            if (row < p.M) store_columns(p.y + static_cast<size_t>(row) * p.N + n, o, n, p.N, p.wide);
+                        } else {
+                            // the lane's 32 values are one MX block of the next layer's K = H
+                            uint32_t cw[kOutE4M3<kOut> ? 8 : 4];
+                            sc_byte = quantize_block<kOutE4M3<kOut>>(o, cw);
+                            if (row < p.M) {
+                                const size_t at = static_cast<size_t>(row) * p.N + n;
+                                if constexpr (kOutE4M3<kOut>) {
+                                    const uint4 a = make_uint4(cw[0], cw[1], cw[2], cw[3]);
+                                    const uint4 b = make_uint4(cw[4], cw[5], cw[6], cw[7]);
+                                    if (p.wide) {
+                                        st_global_v8(p.q_codes + at, a, b);
+                                    } else {
+                                        *reinterpret_cast<uint4*>(p.q_codes + at) = a;
+                                        *reinterpret_cast<uint4*>(p.q_codes + at + 16) = b;
+                                    }
+                                } else {
+                                    *reinterpret_cast<uint4*>(p.q_codes + at / 2) = make_uint4(cw[0], cw[1], cw[2], cw[3]);
+                                }
+                            }
+                        }
                     }
                     if constexpr (kOutQuant<kOut>) store_scale(c, sc_byte);
                 };
@@ -1013,7 +1069,7 @@ __global__ void __launch_bounds__(kThreadsFor<kOut, kQA>, 1)
                 }
             }
         }
-        if (lane == 0) bulk_wait<0>();
+        if (!kOutDirect<kOut> && lane == 0) bulk_wait<0>();
         __syncwarp();
     }
 
@@ -1178,14 +1234,16 @@ int launch_gemm(const GemmArgs& g, cudaStream_t stream, const char** msg, char* 
     }
     // bf16 output (y, or h of the quantizing epilogue): 32 x 32 boxes, 64-byte swizzle
     const void* ybase = g.y ? g.y : g.q_codes;  // without h the map is never used
-    ok = ok && make_map_2d(&my, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, ybase, g.N, g.M, g.N * 2, 32, 32,
-                           CU_TENSOR_MAP_SWIZZLE_64B);
-    if (quant_out) {
+    const bool direct = gated || residual;  // the epilogue stores from registers: no map
+    if (!direct)
+        ok = ok && make_map_2d(&my, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, ybase, g.N, g.M, g.N * 2, 32, 32,
+                               CU_TENSOR_MAP_SWIZZLE_64B);
+    if (quant_out && !direct) {
         // codes of the quantized output: one 32-element block (16 or 32 bytes) x 32 rows per box
         const uint64_t q_row = g.out_fmt == kFmtE4M3 ? g.N : g.N / 2;
         ok = ok && make_map_2d(&mq, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.q_codes, q_row, g.M, q_row,
                                g.out_fmt == kFmtE4M3 ? 32 : 16, 32, CU_TENSOR_MAP_SWIZZLE_NONE);
-    } else {
+    } else if (!direct) {
         mq = my;  // never used by the bf16 epilogue
     }
     // bf16 stages (the low-rank branch, or every stage of a plain bf16 GEMM): operands bf16
@@ -1211,6 +1269,7 @@ int launch_gemm(const GemmArgs& g, cudaStream_t stream, const char** msg, char* 
         mu = ma;  // never used without bf16 stages
         ml = mb;
     }
+    if (direct) my = mq = ml;  // never used
     if (!ok) {
         *msg = "cuTensorMapEncodeTiled failed (driver entry point unavailable or invalid operand layout)";
         return MXQ_ERR_CUDA;
@@ -1241,6 +1300,10 @@ int launch_gemm(const GemmArgs& g, cudaStream_t stream, const char** msg, char* 
     p.qa_atoms_k = quant_a ? static_cast<uint32_t>(sf_atoms_k(g.K)) : 0u;
     p.qa_fmt = quant_a ? g.qa_fmt : -1;
     p.act = g.act;
+    p.y = static_cast<__nv_bfloat16*>(g.y);
+    p.q_codes = static_cast<uint8_t*>(g.q_codes);
+    p.wide = g.N % 16 == 0 && (reinterpret_cast<uintptr_t>(g.y) | reinterpret_cast<uintptr_t>(g.residual) |
+                               reinterpret_cast<uintptr_t>(g.q_codes)) % 32 == 0;
     p.res = static_cast<const __nv_bfloat16*>(g.residual);
     p.gate = g.gate;
     p.gate_f32 = g.gate_f32 ? 1 : 0;

@@ -129,7 +129,7 @@ __device__ __forceinline__ uint32_t gelu_bf16_bits(uint32_t b, const uint16_t* l
 // ---- activations in binary32 ------------------------------------------------------------
 // Applied to the binary32 sum, so that the result is rounded to bf16 once.  The two sigmoid
 // forms v / (1 + exp(-t)) keep their relative accuracy where v is far negative (1 + tanh would
-// cancel there), and the erf form uses erfc for the same reason.
+// cancel there), and so does the erf form, which takes the tail's own function.
 template <int kAct>
 __device__ __forceinline__ float act_f32(float v)
 {
@@ -139,7 +139,20 @@ __device__ __forceinline__ float act_f32(float v)
         constexpr float kTwoRoot = 1.5957691216057308f;  // 2 sqrt(2 / pi)
         return __fdividef(v, 1.0f + __expf(-kTwoRoot * fmaf(0.044715f * v * v, v, v)));
     } else if constexpr (kAct == MXQ_ACT_GELU) {
-        return 0.5f * v * erfcf(v * -0.70710678118654752f);
+        // v Phi(v), with 1 - Phi(a) = exp(-a^2 / 2) q(t) for a = |v| >= 0, t = 1 / (1 + 0.24 a), q a
+        // polynomial of degree 8 (fitted to Mills' ratio over [0, 40], relative error 4.3e-7; the
+        // form is Hastings').  CUDA's erfcf in its place made the epilogue the GEMM's bound.
+        const float t = __fdividef(1.0f, fmaf(0.24f, fabsf(v), 1.0f));
+        float q = -0.0529897924f;
+        q = fmaf(q, t, 0.152786211f);
+        q = fmaf(q, t, -0.0656899739f);
+        q = fmaf(q, t, 0.118377487f);
+        q = fmaf(q, t, 0.0634029045f);
+        q = fmaf(q, t, 0.0928372305f);
+        q = fmaf(q, t, 0.0955223363f);
+        q = fmaf(q, t, 0.0957537846f);
+        const float w = __expf(-0.5f * v * v) * (q * t);
+        return v * (v > 0.0f ? 1.0f - w : w);
     }
     return v;
 }
