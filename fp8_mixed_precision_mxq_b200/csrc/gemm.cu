@@ -860,26 +860,33 @@ __global__ void __launch_bounds__(kThreadsFor<kOut, kQA>, 1)
                     for (int k = 0; k < 4; ++k) {  // 8 columns at a time
                         uint32_t b[4];
                         shfl_bias8(bias8, 4 * c + k, b);
-                        const uint32_t r[4] = {res[k].x, res[k].y, res[k].z, res[k].w};
-                        float gt[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) gt[i] = 1.0f;
-                        if (p.gate != nullptr) {
-                            if (gate_shared) {
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) gt[i] = __shfl_sync(0xFFFFFFFFu, gate8[i], 4 * c + k);
-                            } else if (n + 8 * k < p.N) {  // the warp's rows span two groups
-                                const uint32_t gr = static_cast<uint32_t>(min(res_row, p.M - 1)) / p.rows_per_group;
-                                load_gate8(p.gate, p.gate_f32, static_cast<size_t>(gr) * p.N + n + 8 * k, gt);
-                            }
-                        }
+                        float2 v[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const int e = 8 * k + 2 * i;
-                            const float v0 = act_f32<act>(__uint_as_float(acc[e]) + lo_f(b[i]));
-                            const float v1 = act_f32<act>(__uint_as_float(acc[e + 1]) + hi_f(b[i]));
-                            o[4 * k + i] = bf16x2_bits(fmaf(v0, gt[2 * i], lo_f(r[i])), fmaf(v1, gt[2 * i + 1], hi_f(r[i])));
+                            v[i] = act_f32x2<act>(__fadd2_rn(
+                                make_float2(__uint_as_float(acc[e]), __uint_as_float(acc[e + 1])), make_float2(lo_f(b[i]), hi_f(b[i]))));
                         }
+                        if (p.res != nullptr || p.gate != nullptr) {
+                            const uint32_t r[4] = {res[k].x, res[k].y, res[k].z, res[k].w};
+                            float gt[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) gt[i] = 1.0f;
+                            if (p.gate != nullptr) {
+                                if (gate_shared) {
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i) gt[i] = __shfl_sync(0xFFFFFFFFu, gate8[i], 4 * c + k);
+                                } else if (n + 8 * k < p.N) {  // the warp's rows span two groups
+                                    const uint32_t gr = static_cast<uint32_t>(min(res_row, p.M - 1)) / p.rows_per_group;
+                                    load_gate8(p.gate, p.gate_f32, static_cast<size_t>(gr) * p.N + n + 8 * k, gt);
+                                }
+                            }
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                v[i] = __ffma2_rn(v[i], make_float2(gt[2 * i], gt[2 * i + 1]), make_float2(lo_f(r[i]), hi_f(r[i])));
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) o[4 * k + i] = bf16x2_bits(v[i].x, v[i].y);
                     }
                 });
                 if (res_row < p.M) store_columns(p.y + static_cast<size_t>(res_row) * p.N + n, o, n, p.N, p.wide);
@@ -971,11 +978,12 @@ __global__ void __launch_bounds__(kThreadsFor<kOut, kQA>, 1)
 #pragma unroll
                                 for (int i = 0; i < 4; ++i) {
                                     const int e = 8 * k + 2 * i;
-                                    const float g0 = __uint_as_float(g[e]) + lo_f(bg[i]);
-                                    const float g1 = __uint_as_float(g[e + 1]) + hi_f(bg[i]);
-                                    const float u0 = __uint_as_float(u[e]) + lo_f(bu[i]);
-                                    const float u1 = __uint_as_float(u[e + 1]) + hi_f(bu[i]);
-                                    o[4 * k + i] = bf16x2_bits(act_f32<act>(g0) * u0, act_f32<act>(g1) * u1);
+                                    const float2 gv = act_f32x2<act>(__fadd2_rn(
+                                        make_float2(__uint_as_float(g[e]), __uint_as_float(g[e + 1])), make_float2(lo_f(bg[i]), hi_f(bg[i]))));
+                                    const float2 uv = __fadd2_rn(
+                                        make_float2(__uint_as_float(u[e]), __uint_as_float(u[e + 1])), make_float2(lo_f(bu[i]), hi_f(bu[i])));
+                                    const float2 h = __fmul2_rn(gv, uv);
+                                    o[4 * k + i] = bf16x2_bits(h.x, h.y);
                                 }
                             }
                         });

@@ -127,34 +127,62 @@ __device__ __forceinline__ uint32_t gelu_bf16_bits(uint32_t b, const uint16_t* l
 }
 
 // ---- activations in binary32 ------------------------------------------------------------
-// Applied to the binary32 sum, so that the result is rounded to bf16 once.  The two sigmoid
-// forms v / (1 + exp(-t)) keep their relative accuracy where v is far negative (1 + tanh would
-// cancel there), and so does the erf form, which takes the tail's own function.
+// Applied to the binary32 sum, so that the result is rounded to bf16 once; two values at a time
+// on packed fp32 pairs.  The two sigmoid forms v / (1 + exp(-t)) keep their relative accuracy
+// where v is far negative (1 + tanh would cancel there), and so does the erf form, which takes
+// the tail's own function.
+__device__ __forceinline__ float ex2_approx(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float2 splat(float x) { return make_float2(x, x); }
+
+constexpr float kLog2E = 1.4426950408889634f;
+
+// v / (1 + 2^e)
+__device__ __forceinline__ float2 over_one_plus_exp2(float2 v, float2 e)
+{
+    const float2 d = __fadd2_rn(make_float2(ex2_approx(e.x), ex2_approx(e.y)), splat(1.0f));
+    return make_float2(__fdividef(v.x, d.x), __fdividef(v.y, d.y));
+}
+
 template <int kAct>
-__device__ __forceinline__ float act_f32(float v)
+__device__ __forceinline__ float2 act_f32x2(float2 v)
 {
     if constexpr (kAct == MXQ_ACT_SILU) {
-        return __fdividef(v, 1.0f + __expf(-v));
+        return over_one_plus_exp2(v, __fmul2_rn(v, splat(-kLog2E)));
     } else if constexpr (kAct == MXQ_ACT_GELU_TANH) {
-        constexpr float kTwoRoot = 1.5957691216057308f;  // 2 sqrt(2 / pi)
-        return __fdividef(v, 1.0f + __expf(-kTwoRoot * fmaf(0.044715f * v * v, v, v)));
+        // exp(-2 sqrt(2/pi) (v + 0.044715 v^3)) = 2^(v (c + 0.044715 c v^2))
+        constexpr float c = -1.5957691216057308f * kLog2E;
+        const float2 v2 = __fmul2_rn(v, v);
+        return over_one_plus_exp2(v, __fmul2_rn(v, __ffma2_rn(splat(0.044715f * c), v2, splat(c))));
     } else if constexpr (kAct == MXQ_ACT_GELU) {
         // v Phi(v), with 1 - Phi(a) = exp(-a^2 / 2) q(t) for a = |v| >= 0, t = 1 / (1 + 0.24 a), q a
         // polynomial of degree 8 (fitted to Mills' ratio over [0, 40], relative error 4.3e-7; the
         // form is Hastings').  CUDA's erfcf in its place made the epilogue the GEMM's bound.
-        const float t = __fdividef(1.0f, fmaf(0.24f, fabsf(v), 1.0f));
-        float q = -0.0529897924f;
-        q = fmaf(q, t, 0.152786211f);
-        q = fmaf(q, t, -0.0656899739f);
-        q = fmaf(q, t, 0.118377487f);
-        q = fmaf(q, t, 0.0634029045f);
-        q = fmaf(q, t, 0.0928372305f);
-        q = fmaf(q, t, 0.0955223363f);
-        q = fmaf(q, t, 0.0957537846f);
-        const float w = __expf(-0.5f * v * v) * (q * t);
-        return v * (v > 0.0f ? 1.0f - w : w);
+        const float2 d = __ffma2_rn(splat(0.24f), make_float2(fabsf(v.x), fabsf(v.y)), splat(1.0f));
+        const float2 t = make_float2(__fdividef(1.0f, d.x), __fdividef(1.0f, d.y));
+        float2 q = splat(-0.0529897924f);
+        q = __ffma2_rn(q, t, splat(0.152786211f));
+        q = __ffma2_rn(q, t, splat(-0.0656899739f));
+        q = __ffma2_rn(q, t, splat(0.118377487f));
+        q = __ffma2_rn(q, t, splat(0.0634029045f));
+        q = __ffma2_rn(q, t, splat(0.0928372305f));
+        q = __ffma2_rn(q, t, splat(0.0955223363f));
+        q = __ffma2_rn(q, t, splat(0.0957537846f));
+        const float2 e = __fmul2_rn(__fmul2_rn(v, v), splat(-0.5f * kLog2E));
+        const float2 w = __fmul2_rn(make_float2(ex2_approx(e.x), ex2_approx(e.y)), __fmul2_rn(q, t));
+        return __fmul2_rn(v, make_float2(v.x > 0.0f ? 1.0f - w.x : w.x, v.y > 0.0f ? 1.0f - w.y : w.y));
     }
     return v;
+}
+
+template <int kAct>
+__device__ __forceinline__ float act_f32(float v)
+{
+    return act_f32x2<kAct>(make_float2(v, v)).x;
 }
 
 // f(integral constant of the activation): the choice is taken once, outside f's loops.
