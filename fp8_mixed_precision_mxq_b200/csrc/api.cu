@@ -282,8 +282,8 @@ void set_epilogue(GemmArgs& g, const mxq_epilogue& e)
 int run_epilogue_gemm(const GemmArgs& g, const char* what, cudaStream_t stream)
 {
     const char* msg = nullptr;
-    int rc = g.M <= kRowsMaxM ? launch_gemm_rows(g, stream, &msg, g_path, sizeof g_path)
-                              : launch_gemm(g, stream, &msg, g_path, sizeof g_path);
+    int rc = few_rows(g) ? launch_gemm_rows(g, stream, &msg, g_path, sizeof g_path)
+                         : launch_gemm(g, stream, &msg, g_path, sizeof g_path);
     if (rc != MXQ_OK) return fail(rc, "%s: %s", what, msg ? msg : "launch failed");
     return ok();
 }
@@ -1111,7 +1111,7 @@ int mxq_gated_ffn(const void* x_bf16, int64_t M, int64_t K, const mxq_wdesc* gat
     char gp[sizeof g_path];
     snprintf(gp, sizeof gp, "%s", g_path);
     RETURN_IF(run_gemm_residual(hc, hs, down_fmt, M, H, down->codes, down->sf, down->N, down->bias, *e, y_bf16, st,
-                                nullptr, M <= kRowsMaxM));
+                                nullptr, M <= kRowsTileM));
     char dp[sizeof g_path];
     snprintf(dp, sizeof dp, "%s", g_path);
     snprintf(g_path, sizeof g_path, "gated ffn: %.110s | %.110s", gp, dp);

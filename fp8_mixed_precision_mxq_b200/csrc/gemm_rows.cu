@@ -1,9 +1,9 @@
-// gemm_rows.cu -- the residual and gated GEMMs for a few activation rows (up to 64): one
-// token, or a batch of decoding sequences.
+// gemm_rows.cu -- the residual and gated GEMMs for few activation rows: one token, a batch of
+// decoding sequences, a short prompt (few_rows in mxq_internal.h draws the line).
 //
 // With few rows the weight is all there is to read (0.53 bytes per element), so the MMA's
 // 128-row operand is the weight and its N dimension the tokens: D[n, t] = sum_k W[n, k] x[t, k].
-// A 128-row weight tile and one range of K belong to a CTA; the S CTAs of a cluster split K
+// A 128-row weight tile, up to 64 tokens and one range of K belong to a CTA; the S CTAs of a cluster split K
 // and add their partial sums through distributed shared memory, so that every SM streams
 // weights even when there are few tiles.  Two CTAs fit an SM.
 //   warp 0      TMA producer: weight tile(s), activation rows and their scale atoms into the
@@ -209,12 +209,14 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int split = gridDim.x;  // the cluster: one CTA per range of K (a power of two)
     const int rank = blockIdx.x;
     const int tile = blockIdx.y;
+    const int m0 = blockIdx.z * kNT;       // the CTA's tokens
+    const int M = min(kNT, p.M - m0);
     const int ks0 = static_cast<int>(static_cast<int64_t>(p.k_stages) * rank / split);
     const int ks1 = static_cast<int>(static_cast<int64_t>(p.k_stages) * (rank + 1) / split);
     const int n_stages = ks1 - ks0;
     const int n_first = min(S, n_stages);  // the ring starts out empty
     // debug: leave one stage unfilled, so that the MMA wait runs out
-    const int skipped = (p.debug & 1u) && rank == 0 && tile == 0 ? 0 : -1;
+    const int skipped = (p.debug & 1u) && rank == 0 && tile == 0 && m0 == 0 ? 0 : -1;
 
     // one operand's scale bytes in the CTA's stage `it` (the last stage of K may have fewer atoms)
     auto sf_bytes_of = [&](int it) {
@@ -224,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     // operand o's scales (0, 1: the weights; kW: the activation) of a stage: one contiguous run
     auto load_sf = [&](int o, int it) {
         const uint8_t* base = o == C::kW ? p.sf_x : o == 0 ? p.sf_w : p.sf_w2;
-        const size_t row = o == C::kW ? 0 : static_cast<size_t>(tile) * p.atoms_k * 512u;
+        const size_t row = static_cast<size_t>(o == C::kW ? m0 / 128 : tile) * p.atoms_k * 512u;
         bulk_load(smem + C::kOffSf + (o * S + it % S) * C::kSf, base + row + static_cast<size_t>(ks0 + it) * C::kSf,
                   sf_bytes_of(it), smem_u32(&full[it % S]));
     };
@@ -241,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         if constexpr (kGated) tma_load_2d<1>(st + C::kTileW, &map_w2, kx, tile * 128, bar, pol);
     };
     auto load_x = [&](int it, uint64_t pol) {
-        tma_load_2d<1>(smem + it % S * C::kStage + C::kOffX, &map_x, (ks0 + it) * (kKind == kBf16 ? 64 : 128), 0,
+        tma_load_2d<1>(smem + it % S * C::kStage + C::kOffX, &map_x, (ks0 + it) * (kKind == kBf16 ? 64 : 128), m0,
                        smem_u32(&full[it % S]), pol);
     };
 
@@ -300,18 +302,18 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int t = 4 * a + i;
-            if (kGated || !live || t >= p.M) continue;
+            if (kGated || !live || t >= M) continue;
             if (p.gate != nullptr) {
-                const size_t gi = static_cast<size_t>(static_cast<uint32_t>(t) / p.rows_per_group) * p.N + n;
+                const size_t gi = static_cast<size_t>(static_cast<uint32_t>(m0 + t) / p.rows_per_group) * p.N + n;
                 gate4[i] = p.gate_f32 ? __ldg(static_cast<const float*>(p.gate) + gi)
                                       : __bfloat162float(static_cast<const __nv_bfloat16*>(p.gate)[gi]);
             }
-            if (p.res != nullptr) res4[i] = __bfloat162float(p.res[static_cast<size_t>(t) * p.N + n]);
+            if (p.res != nullptr) res4[i] = __bfloat162float(p.res[static_cast<size_t>(m0 + t) * p.N + n]);
         }
     };
     // what the last step needs from memory, fetched while the weight streams
     auto load_epilogue = [&]() {
-        if (!live || 4 * first4 >= p.M) return;
+        if (!live || 4 * first4 >= M) return;
         if (p.bias != nullptr) b0 = __bfloat162float(p.bias[n]);
         if (kGated && p.bias2 != nullptr) b1 = __bfloat162float(p.bias2[n]);
         load_four(first4);
@@ -367,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 tc_fence_after();
                 const uint32_t st = smem_u32(smem + s * C::kStage);
                 const uint32_t w_lo = sdesc_sw128_lo(st), x_lo = sdesc_sw128_lo(st + C::kOffX);
-                const uint32_t tsf = tmem + C::kSfCol + s * C::kSfCols;
+                const uint32_t tsf = tmem + C::kSfCol + s * C::kSfCols;  // 32 rows of an operand to a column
                 const int kvalid = p.K - ks * C::kKps;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -384,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                                 mma_block_scaled<1, kKind == kMxf8>(
                                     tmem + w * kNT, wd, x_lo + 2 * j, kSdescSw128Hi,
                                     idesc_block_scaled(fw, fx, 128, kNT, id, id), tsf + 4 * (w * C::kAtoms + atom),
-                                    tsf + 4 * (C::kW * C::kAtoms + atom), accum);
+                                    tsf + 4 * (C::kW * C::kAtoms + atom) + (m0 & 127) / 32, accum);
                         }
                     }
                 }
@@ -459,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int w = 0; w < C::kW; ++w)
 #pragma unroll 1
             for (int t0 = 0; t0 < kNT; t0 += 16) {
-                if (t0 >= p.M) break;
+                if (t0 >= M) break;
                 uint32_t r[16];
                 tmem_ld_x16(tmem + (static_cast<uint32_t>(q * 32) << 16) + w * kNT + t0, r);
                 tmem_ld_wait();
@@ -480,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
     for (int r = 0; r < kMaxSplit; ++r)
         if (r < split) bad |= ld_cluster_u32(mapa_shared(smem_u32(failed), r));
-    const int fours = (p.M + 3) / 4;
+    const int fours = (M + 3) / 4;
     if (warp < 2) {  // these two had other work until now
         grid_wait();
         load_epilogue();
@@ -514,12 +516,12 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int t = 4 * a + i;
-                    if (t >= p.M) break;
+                    if (t >= M) break;
                     float o = act_f32<act>(s0[i] + b0);
                     if constexpr (kGated) o *= s1[i] + b1;
                     else o = fmaf(o, gate4[i], res4[i]);
                     if (!kGated || p.out_fmt == MXQ_OUT_BF16) {
-                        if (live) p.y[static_cast<size_t>(t) * p.N + n] = __float2bfloat16_rn(o);
+                        if (live) p.y[static_cast<size_t>(m0 + t) * p.N + n] = __float2bfloat16_rn(o);
                         continue;
                     }
                     // h: the warp's 32 values of this token are one MX block (N is a multiple of 32)
@@ -532,41 +534,41 @@ __global__ void __launch_bounds__(kThreads, 2)
                         const float q = lo_f(hb) * e8m0_inverse(sc);
                         const float q1 = __shfl_down_sync(0xFFFFFFFFu, q, 1);
                         if (e4m3) {
-                            p.q_codes[static_cast<size_t>(t) * p.N + n] =
+                            p.q_codes[static_cast<size_t>(m0 + t) * p.N + n] =
                                 sc == 255u ? uint8_t(0) : static_cast<uint8_t>(cvt_e4m3x2(q, 0.0f) & 0xFFu);
                         } else if ((lane & 1) == 0) {
                             const float pair[8] = {q, q1, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                            p.q_codes[(static_cast<size_t>(t) * p.N + n) / 2] =
+                            p.q_codes[(static_cast<size_t>(m0 + t) * p.N + n) / 2] =
                                 sc == 255u ? uint8_t(0) : static_cast<uint8_t>(cvt_e2m1x8(pair) & 0xFFu);
                         }
                     }
                     if (lane == 0)  // this token's scale byte (0 for the padding past N)
-                        p.q_sf[sf_word(t, tile, p.atoms_n) + (warp & 3)] = static_cast<uint8_t>(sc);
+                        p.q_sf[sf_word(m0 + t, tile, p.atoms_n) + (warp & 3)] = static_cast<uint8_t>(sc);
                 }
             }
         });
     // the layout's padding rows, one word of this tile each
-    if (kGated && p.out_fmt != MXQ_OUT_BF16 && rank == 0 && bad == 0u)
-        for (int t = p.M + static_cast<int>(threadIdx.x); t < 128; t += kThreads)
+    if (kGated && p.out_fmt != MXQ_OUT_BF16 && rank == 0 && bad == 0u && m0 + kNT >= p.M)
+        for (int t = p.M + static_cast<int>(threadIdx.x); t < (p.M + 127) / 128 * 128; t += kThreads)
             *reinterpret_cast<uint32_t*>(p.q_sf + sf_word(t, tile, p.atoms_n)) = 0u;
     cluster_wait();  // no CTA leaves while another may read its partials
 }
 
 template <int kKind, bool kGated, int kNT, bool kQX>
-cudaError_t launch_rows(const CUtensorMap (&m)[3], const RowsParams& p, int split, int tiles, cudaStream_t stream)
+cudaError_t launch_rows(const CUtensorMap (&m)[3], const RowsParams& p, dim3 grid, cudaStream_t stream)
 {
     using C = Cfg<kKind, kGated, kNT>;
     auto kern = gemm_rows_kernel<kKind, kGated, kNT, kQX>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(split, tiles, 1);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(kThreads, 1, 1);
     cfg.dynamicSmemBytes = C::kSmem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = split;
+    attr[0].val.clusterDim.x = grid.x;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -577,22 +579,22 @@ cudaError_t launch_rows(const CUtensorMap (&m)[3], const RowsParams& p, int spli
 }
 
 template <int kKind, bool kGated>
-cudaError_t launch_nt(int nt, const CUtensorMap (&m)[3], const RowsParams& p, int split, int tiles,
+cudaError_t launch_nt(int nt, const CUtensorMap (&m)[3], const RowsParams& p, dim3 grid,
                       cudaStream_t stream)
 {
     if constexpr (kKind != kBf16)
-        if (p.x != nullptr) return launch_rows<kKind, kGated, 16, true>(m, p, split, tiles, stream);
-    if (nt == 16) return launch_rows<kKind, kGated, 16, false>(m, p, split, tiles, stream);
-    if (nt == 32) return launch_rows<kKind, kGated, 32, false>(m, p, split, tiles, stream);
-    return launch_rows<kKind, kGated, 64, false>(m, p, split, tiles, stream);
+        if (p.x != nullptr) return launch_rows<kKind, kGated, 16, true>(m, p, grid, stream);
+    if (nt == 16) return launch_rows<kKind, kGated, 16, false>(m, p, grid, stream);
+    if (nt == 32) return launch_rows<kKind, kGated, 32, false>(m, p, grid, stream);
+    return launch_rows<kKind, kGated, 64, false>(m, p, grid, stream);
 }
 
 template <int kKind>
-cudaError_t launch_kind(bool gated, int nt, const CUtensorMap (&m)[3], const RowsParams& p, int split, int tiles,
+cudaError_t launch_kind(bool gated, int nt, const CUtensorMap (&m)[3], const RowsParams& p, dim3 grid,
                         cudaStream_t stream)
 {
-    return gated ? launch_nt<kKind, true>(nt, m, p, split, tiles, stream)
-                 : launch_nt<kKind, false>(nt, m, p, split, tiles, stream);
+    return gated ? launch_nt<kKind, true>(nt, m, p, grid, stream)
+                 : launch_nt<kKind, false>(nt, m, p, grid, stream);
 }
 
 }  // namespace
@@ -605,6 +607,24 @@ int read_and_clear_rows_status(cudaStream_t stream, uint32_t* out)
     if (cudaMemcpyToSymbol(g_rows_status, &zero, sizeof zero) != cudaSuccess) return MXQ_ERR_CUDA;
     *out = v;
     return MXQ_OK;
+}
+
+namespace {
+
+int num_sms()
+{
+    int dev = 0, sms = 148;
+    if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    return sms;
+}
+
+}  // namespace
+
+bool few_rows(const GemmArgs& g)
+{
+    if (g.M <= kRowsTileM) return true;
+    const int64_t tiles = ceil_div(g.M, kRowsTileM) * ceil_div(g.N, 128);
+    return tiles * (g.epilogue == kEpilogueGated ? 2 : 1) <= num_sms();
 }
 
 int launch_gemm_rows(const GemmArgs& g, cudaStream_t stream, const char** msg, char* path, size_t path_len)
@@ -664,16 +684,15 @@ int launch_gemm_rows(const GemmArgs& g, cudaStream_t stream, const char** msg, c
     p.q_codes = static_cast<uint8_t*>(g.q_codes);
     p.q_sf = static_cast<uint8_t*>(g.q_sf);
 
-    int dev = 0, sms = 148;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     // K is split while all CTAs still run at once, two to an SM
-    const int tiles = static_cast<int>(ceil_div(g.N, 128));
+    const int sms = num_sms();
+    const int tiles = static_cast<int>(ceil_div(g.N, 128) * ceil_div(g.M, nt));
     int split = 1;
     while (split < kMaxSplit && 2 * split * tiles <= 2 * sms && 2 * split <= p.k_stages) split *= 2;
-    cudaError_t e = kind == kBf16   ? launch_kind<kBf16>(gated, nt, m, p, split, tiles, stream)
-                    : kind == kMxf8 ? launch_kind<kMxf8>(gated, nt, m, p, split, tiles, stream)
-                                    : launch_kind<kMxf4>(gated, nt, m, p, split, tiles, stream);
+    const dim3 grid(split, static_cast<unsigned>(ceil_div(g.N, 128)), static_cast<unsigned>(ceil_div(g.M, nt)));
+    cudaError_t e = kind == kBf16   ? launch_kind<kBf16>(gated, nt, m, p, grid, stream)
+                    : kind == kMxf8 ? launch_kind<kMxf8>(gated, nt, m, p, grid, stream)
+                                    : launch_kind<kMxf4>(gated, nt, m, p, grid, stream);
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) {
         *msg = cudaGetErrorString(e);

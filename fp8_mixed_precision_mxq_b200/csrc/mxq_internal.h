@@ -99,7 +99,7 @@ struct GemmArgs {
     const void* w2_codes = nullptr;
     const void* w2_sf = nullptr;
     const void* bias2 = nullptr;
-    // few-row kernel only.  x: the activation in bf16 (M <= kRowsMaxQuantM), quantized to a_fmt
+    // few-row kernel only (M <= kRowsTileM).  x: the activation in bf16 (M <= kRowsMaxQuantM), quantized to a_fmt
     // inside the kernel; a_codes and a_sf are not read.  early: the kernel before on the stream
     // is this library's, launched behind everything that wrote the weight.
     const void* x = nullptr;
@@ -112,9 +112,15 @@ int launch_gemm(const GemmArgs& g, cudaStream_t stream, const char** msg, char* 
 
 const char* epilogue_name(const GemmArgs& g);  // for the path description
 
-// The residual or gated GEMM for at most kRowsMaxM activation rows (gemm_rows.cu); arguments
-// and results as launch_gemm's.
-constexpr int64_t kRowsMaxM = 64;
+// The residual or gated GEMM for few activation rows (gemm_rows.cu); arguments and results as
+// launch_gemm's.  It takes up to kRowsTileM rows of any output, and more where the output has no
+// more 128 x kRowsTileM tiles (counting both weights of a gated pair) than the GPU has SMs: one
+// wave of them ends before the pair kernel's 256 x 256 tiles, which leave most SMs idle there.
+// Measured (us, this kernel / the pair kernel): W4A4 residual 5120 x 5120 at 192 rows (120 tiles)
+// 11.7 / 17.0, at 256 (160) 17.6 / 17.2; W4A8 K = 13824 at 192 rows 27 / 53; gated 5120 x 5120
+// W4A4 at 64 rows (80) 12.7 / 15.9, at 128 (160) 16.8 / 15.9; 1024 x 1024 at 1024 rows (128) 7.9 / 10.6.
+constexpr int64_t kRowsTileM = 64;
+bool few_rows(const GemmArgs& g);
 constexpr int64_t kRowsMaxQuantM = 16;
 int launch_gemm_rows(const GemmArgs& g, cudaStream_t stream, const char** msg, char* path, size_t path_len);
 

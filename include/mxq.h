@@ -455,9 +455,10 @@ typedef struct {
 } mxq_epilogue;
 
 /* mxq_gemm with activation, gate and residual in its epilogue.  Arguments and limits as for
- * mxq_gemm; residual and gate 16-byte aligned.  Up to 64 rows run on a kernel of their own that
- * streams the weight (the tokens are the MMA's N dimension, K is split over a cluster); its
- * sums are formed in another order than the large kernel's. */
+ * mxq_gemm; residual and gate 16-byte aligned.  Few rows (64, or more of an output with few
+ * tiles) run on a kernel of their own that streams the weight (the tokens are the MMA's N
+ * dimension, K is split over a cluster); its sums are formed in another order than the large
+ * kernel's. */
 int mxq_gemm_residual(const void* a_codes, const void* a_sf, int a_fmt, int64_t M, int64_t K, const void* w_codes,
                       const void* w_sf, int64_t N, const void* bias_bf16, const mxq_epilogue* e, void* y_bf16,
                       void* stream);

@@ -106,7 +106,14 @@ def weight(g, N, K, bias=True, std=0.05):
     return q, deq(q.codes, q.sf, N, K, "e2m1")
 
 
-# M: the few-row kernel's three widths and both sides of their borders, then pairs
+def on_few_rows(M, N, gated=False):
+    """The library's choice of kernel: few rows, or an output of at most an SM count of tiles."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    return M <= 64 or -(-M // 64) * -(-N // 128) * (2 if gated else 1) <= sms
+
+
+# The few-row kernel's widths and both sides of its borders (16, 32 and 64 tokens; several token
+# tiles), and the pair kernel, ragged in every direction
 RESIDUAL = [  # M, N, K, fmt, act, bias, residual, gate groups, gate dtype
     (1, 8, 32, "e2m1", "none", False, False, 0, None),
     (1, 5120, 5120, "e2m1", "none", True, True, 1, torch.float32),
@@ -118,10 +125,13 @@ RESIDUAL = [  # M, N, K, fmt, act, bias, residual, gate groups, gate dtype
     (64, 4104, 2048, "e2m1", "silu", True, False, 1, torch.float32),
     (64, 512, 5120, "e4m3", "gelu", True, True, 64, torch.float32),
     (65, 256, 512, "e2m1", "none", True, True, 1, torch.float32),
-    (128, 8, 32, "e2m1", "none", False, True, 0, None),
-    (129, 520, 256, "e4m3", "gelu", True, True, 3, torch.bfloat16),   # groups that end inside a warp's rows
-    (300, 1056, 1024, "e2m1", "gelu_tanh", True, False, 0, None),
-    (513, 264, 2048, "e4m3", "silu", True, True, 513, torch.float32),  # a group for each row
+    (130, 520, 5120, "e2m1", "gelu", True, True, 3, torch.bfloat16),
+    (200, 2056, 1024, "e4m3", "silu", True, True, 2, torch.float32),
+    (1000, 264, 544, "e2m1", "none", True, True, 7, torch.float32),
+    (65, 9608, 32, "e2m1", "none", False, True, 0, None),
+    (129, 6408, 256, "e4m3", "gelu", True, True, 3, torch.bfloat16),   # groups that end inside a warp's rows
+    (300, 4104, 1024, "e2m1", "gelu_tanh", True, False, 0, None),
+    (513, 2200, 2048, "e4m3", "silu", True, True, 513, torch.float32),  # a group for each row
     (1000, 5120, 1280, "e2m1", "none", True, True, 2, torch.float32),
 ]
 
@@ -137,7 +147,7 @@ def test_gemm_residual_against_float64(M, N, K, fmt, act, bias, residual, groups
     rpg = -(-M // max(1, groups))
     y = ops.gemm_residual(*a, w, act=act, residual=r, gate=gate, rows_per_group=rpg)
     assert ops.poll_status() == 0
-    assert ("rows" in ops.last_path()) == (M <= 64) and "+act+residual" in ops.last_path()
+    assert ops.last_path().startswith("rows") == on_few_rows(M, N) and "+act+residual" in ops.last_path()
     check_residual(y, a64, w64, w.bias, act, r, gate, rpg, "M=%d N=%d K=%d %s %s" % (M, N, K, fmt, act))
     # in place of the residual: the same bits
     if residual:
@@ -147,8 +157,8 @@ def test_gemm_residual_against_float64(M, N, K, fmt, act, bias, residual, groups
 
 @pytest.mark.parametrize("M,N,K,act,groups", [
     (1, 8, 8, "none", 1), (5, 136, 72, "gelu", 2), (16, 5120, 4096, "none", 0), (40, 264, 1000, "silu", 1),
-    (64, 128, 64, "gelu_tanh", 1), (65, 520, 136, "gelu_tanh", 0), (512, 5120, 4096, "gelu_tanh", 0),
-    (300, 264, 2056, "silu", 7),
+    (64, 128, 64, "gelu_tanh", 1), (65, 520, 136, "gelu_tanh", 0), (170, 1032, 264, "gelu", 4),
+    (512, 5120, 4096, "gelu_tanh", 0), (300, 4104, 2056, "silu", 7), (129, 6424, 136, "gelu", 0),
 ])
 def test_gemm_bf16_residual_against_float64(M, N, K, act, groups):
     ops = _ops()
@@ -168,7 +178,7 @@ def test_plain_epilogue_is_the_plain_gemm():
     g = gen(1)
     for fmt in ("e2m1", "e4m3"):
         a, _ = operand(g, 300, 1024, fmt)
-        w, _ = weight(g, 520, 1024)
+        w, _ = weight(g, 4104, 1024)
         assert torch.equal(ops.gemm_residual(*a, w), ops.gemm(*a, w))
 
 
@@ -196,8 +206,10 @@ GATED = [  # M, H, K, fmt, act, bias
     (64, 2080, 1280, "e4m3", "silu", True),
     (65, 128, 256, "e2m1", "silu", False),
     (100, 8, 32, "e2m1", "gelu", True),
-    (257, 1056, 512, "e4m3", "gelu_tanh", True),
-    (300, 96, 544, "e2m1", "gelu", True),
+    (200, 1056, 512, "e4m3", "gelu_tanh", True),   # token tiles that share a scale atom
+    (65, 4768, 544, "e2m1", "gelu", True),
+    (300, 2080, 32, "e2m1", "gelu", True),
+    (257, 2088, 512, "e4m3", "gelu_tanh", True),
     (777, 5632, 2048, "e4m3", "silu", True),
 ]
 
@@ -210,6 +222,7 @@ def test_gemm_gated_against_float64(M, H, K, fmt, act, bias):
     (wg, g64), (wu, u64) = weight(g, H, K, bias), weight(g, H, K, bias)
     h = ops.gemm_gated(*a, wg, wu, act=act)
     assert ops.poll_status() == 0 and "+gated->bf16" in ops.last_path()
+    assert ops.last_path().startswith("rows") == on_few_rows(M, H, gated=True)
     check_gated(h, a64, g64, wg.bias, u64, wu.bias, act, "M=%d H=%d K=%d %s %s" % (M, H, K, fmt, act))
     if H % 32 == 0:
         for of in ("e2m1", "e4m3"):  # the bits of the activation quantizer, padding included
@@ -222,7 +235,7 @@ def test_gemm_gated_against_float64(M, H, K, fmt, act, bias):
 
 
 @pytest.mark.parametrize("M,H,K", [(1, 8, 8), (3, 160, 72), (50, 544, 1000), (64, 128, 2048), (70, 264, 136),
-                                   (300, 1056, 512)])
+                                   (150, 544, 512), (300, 2080, 512)])
 def test_gemm_bf16_gated_against_float64(M, H, K):
     ops = _ops()
     g = gen(M + H + K)
@@ -238,12 +251,12 @@ def test_gemm_bf16_gated_against_float64(M, H, K):
             assert torch.equal(codes, want_c) and torch.equal(sf, want_s), of
 
 
-@pytest.mark.parametrize("M", [1, 20, 64, 65, 333])
+@pytest.mark.parametrize("M", [1, 20, 64, 65, 333, 2100])
 @pytest.mark.parametrize("up_fmt,down_fmt", [("e2m1", "e4m3"), ("e4m3", "e2m1")])
 def test_gated_ffn_is_its_steps(M, up_fmt, down_fmt):
     ops = _ops()
     g = gen(M)
-    K, H = 640, 1152
+    K, H = 640, 3200
     x, r, gate = normal(g, M, K), normal(g, M, K), normal(g, 1, K, dtype=torch.float32)
     (wg, _), (wu, _), (wd, d64) = weight(g, H, K), weight(g, H, K), weight(g, K, H)
     c, s = ops.quantize_act(x, up_fmt)
@@ -254,7 +267,7 @@ def test_gated_ffn_is_its_steps(M, up_fmt, down_fmt):
     check_residual(y, deq(hc, hs, M, H, down_fmt), d64, wd.bias, "none", r, gate, M, "gated ffn M=%d" % M)
 
 
-@pytest.mark.parametrize("M", [1, 65, 700])
+@pytest.mark.parametrize("M", [1, 65, 1500])
 def test_block_norm_gated_ffn_residual(M):
     """The operators as a block uses them: the fused norm writes the operand, the gated GEMM
     the hidden operand, and the last linear adds its gated result to the stream, in place."""
@@ -273,7 +286,7 @@ def test_block_norm_gated_ffn_residual(M):
     assert out is z and torch.equal(out, want) and ops.poll_status() == 0
 
 
-@pytest.mark.parametrize("M", [3, 200])
+@pytest.mark.parametrize("M", [3, 200, 9700])
 def test_nonfinite_rows_stay_in_their_rows(M):
     """A NaN in one row's input makes that row NaN (E8M0 code 255) and no other."""
     ops = _ops()
@@ -297,7 +310,7 @@ def test_large_sums_reach_infinity_and_saturated_activations():
     """Sums far out in both tails: silu and both GELUs give v for large v and a (signed) zero
     for far negative v, no NaN."""
     ops = _ops()
-    for M in (4, 100):
+    for M in (4, 100, 9700):
         x = torch.full((M, 64), 30.0, device="cuda").bfloat16()
         w = torch.ones((16, 64), device="cuda").bfloat16()
         w[8:] = -1
@@ -306,7 +319,7 @@ def test_large_sums_reach_infinity_and_saturated_activations():
             assert (y[:, :8] == 1920).all() and (y[:, 8:] == 0).all(), act
 
 
-@pytest.mark.parametrize("M", [8, 300])
+@pytest.mark.parametrize("M", [8, 300, 3000])
 def test_captured_replayed_and_on_two_streams(M):
     ops = _ops()
     g = gen(M)
@@ -338,7 +351,7 @@ def test_captured_replayed_and_on_two_streams(M):
     assert all(torch.equal(o, want) for o in outs) and ops.poll_status() == 0
 
 
-@pytest.mark.parametrize("M", [8, 300])
+@pytest.mark.parametrize("M", [8, 300, 5000])
 def test_a_wait_that_runs_out_is_reported(M):
     """Debug bit 0: a stage is never filled; the kernel's wait ends after its limit, the status
     says so, and the next call is right again."""
