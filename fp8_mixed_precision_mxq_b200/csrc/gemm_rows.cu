@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const int split = gridDim.x;  // the cluster: one CTA per range of K (a power of two)
+    const int split = gridDim.x;  // the cluster: one CTA per range of K
     const int rank = blockIdx.x;
     const int tile = blockIdx.y;
     const int m0 = blockIdx.z * kNT;       // the CTA's tokens
