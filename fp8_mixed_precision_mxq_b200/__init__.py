@@ -5,6 +5,6 @@ and tcgen05 block-scaled GEMMs) behind the C ABI of include/mxq.h; this package 
 the Python binding of that ABI.
 """
 from ._lib import FMT_E2M1, FMT_E4M3, MODE_NATIVE, MODE_QDQ, MxqError, lib  # noqa: F401
-from .ops import (QWeight, block_workspace_bytes, codes_bytes, dequantize, dit_block_linears, gemm,  # noqa: F401
-                  last_path, linear, poll_status, quantize_act, quantize_weight, set_debug, sf_bytes,
-                  sf_to_logical, workspace_bytes)
+from .ops import (QWeight, block_workspace_bytes, codes_bytes, dequantize, dit_block_linears, gated_ffn,  # noqa: F401
+                  gemm, gemm_gated, gemm_residual, last_path, linear, linear_residual, norm_residual, poll_status,
+                  quantize_act, quantize_weight, set_debug, sf_bytes, sf_to_logical, workspace_bytes)
