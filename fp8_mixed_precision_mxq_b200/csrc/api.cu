@@ -1031,15 +1031,19 @@ int mxq_linear_residual(const void* x_bf16, int64_t M, int64_t K, const void* w_
     // x stands in for the quantized activation in the GEMM checks
     RETURN_IF(check_gemm(x_bf16, x_bf16, act_fmt, M, K, w_codes, w_sf, N, bias_bf16, y_bf16));
     RETURN_IF(check_epilogue(e));
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (fused) {
-        RETURN_IF(check_device());
-        return run_gemm_residual(nullptr, nullptr, act_fmt, M, K, w_codes, w_sf, N, bias_bf16, *e, y_bf16, st, x_bf16);
+    if (!fused) {
+        const int64_t need = linear_ws(M, N, K, act_fmt, MXQ_MODE_NATIVE);
+        if (ws_bytes < need)
+            return fail(MXQ_ERR_WORKSPACE, "workspace has %lld bytes, needs %lld", (long long)ws_bytes, (long long)need);
     }
-    const int64_t need = linear_ws(M, N, K, act_fmt, MXQ_MODE_NATIVE);
-    if (ws_bytes < need)
-        return fail(MXQ_ERR_WORKSPACE, "workspace has %lld bytes, needs %lld", (long long)ws_bytes, (long long)need);
+    // the fused kernel's CTAs read x while others write y
+    const uintptr_t xa = reinterpret_cast<uintptr_t>(x_bf16), ya = reinterpret_cast<uintptr_t>(y_bf16);
+    if (xa < ya + static_cast<uint64_t>(M) * N * 2 && ya < xa + static_cast<uint64_t>(M) * K * 2)
+        return fail(MXQ_ERR_INVALID_ARG, "linear with residual: y overlaps x");
     RETURN_IF(check_device());
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (fused)
+        return run_gemm_residual(nullptr, nullptr, act_fmt, M, K, w_codes, w_sf, N, bias_bf16, *e, y_bf16, st, x_bf16);
     uint8_t* xc = static_cast<uint8_t*>(workspace);
     uint8_t* xs = xc + round_up(codes_bytes(M, K, act_fmt), kWsAlign);
     RETURN_IF(cuda_rc(launch_quantize(x_bf16, M, K, act_fmt, xc, xs, st), "quantize launch"));

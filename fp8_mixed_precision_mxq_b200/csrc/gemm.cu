@@ -227,7 +227,6 @@ struct Params {
     const __nv_bfloat16* bias2;
 };
 
-
 // Eight gate values (fp32 or bf16) from element i on.
 __device__ __forceinline__ void load_gate8(const void* gate, int f32, size_t i, float (&v)[8])
 {
@@ -800,44 +799,42 @@ __global__ void __launch_bounds__(kThreadsFor<kOut, kQA>, 1)
             // block's scale byte
             auto emit = [&](const uint32_t(&o)[16], int n) __attribute__((always_inline)) -> uint32_t {
                 uint32_t sc_byte = 0u;
-                                    const bool store_y = kOut == kOutBf16 || (kOutEbuf<kOut> && p.write_h);
-                                    uint8_t* buf = ebuf0 + eb * kEpiBuf;
-                                    // the stores that last used this chunk's buffers have read them
-                                    if (lane == 0) {
-                                        if constexpr (C::kQBufs == 1)
-                                            bulk_wait_read<0>();
-                                        else
-                                            bulk_wait_read<1>();
-                                    }
-                                    __syncwarp();
-                                    if (kOutEbuf<kOut> && store_y) {
-                                        const uint32_t rsw = (static_cast<uint32_t>(lane) >> 1) & 3u;
-                #pragma unroll
-                                        for (int ch = 0; ch < 4; ++ch) {
-                                            uint4* dst = reinterpret_cast<uint4*>(buf + lane * 64 + ((ch ^ rsw) * 16));
-                                            *dst = make_uint4(o[4 * ch], o[4 * ch + 1], o[4 * ch + 2], o[4 * ch + 3]);
-                                        }
-                                    }
-                                    if constexpr (kOutQuant<kOut>) {
-                                        // this lane's 32 values are one MX block of the next layer's K
-                    uint8_t* qb = qbuf0 + (C::kQBufs == 2 ? eb : 0) * C::kQBuf;
+                const bool store_y = kOut == kOutBf16 || (kOutEbuf<kOut> && p.write_h);
+                uint8_t* buf = ebuf0 + eb * kEpiBuf;
+                uint8_t* qb = qbuf0 + (C::kQBufs == 2 ? eb : 0) * C::kQBuf;
+                // the stores that last used this chunk's buffers have read them
+                if (lane == 0) {
+                    if constexpr (C::kQBufs == 1)
+                        bulk_wait_read<0>();
+                    else
+                        bulk_wait_read<1>();
+                }
+                __syncwarp();
+                if (kOutEbuf<kOut> && store_y) {
+                    const uint32_t rsw = (static_cast<uint32_t>(lane) >> 1) & 3u;
+#pragma unroll
+                    for (int ch = 0; ch < 4; ++ch) {
+                        uint4* dst = reinterpret_cast<uint4*>(buf + lane * 64 + ((ch ^ rsw) * 16));
+                        *dst = make_uint4(o[4 * ch], o[4 * ch + 1], o[4 * ch + 2], o[4 * ch + 3]);
+                    }
+                }
+                if constexpr (kOutQuant<kOut>) {
+                    // this lane's 32 values are one MX block of the next layer's K
                     uint32_t cw[kOutE4M3<kOut> ? 8 : 4];
                     sc_byte = quantize_block<kOutE4M3<kOut>>(o, cw);
 #pragma unroll
                     for (int k = 0; k < (kOutE4M3<kOut> ? 2 : 1); ++k)
                         *reinterpret_cast<uint4*>(qb + lane * (kOutE4M3<kOut> ? 32 : 16) + 16 * k) =
                             make_uint4(cw[4 * k], cw[4 * k + 1], cw[4 * k + 2], cw[4 * k + 3]);
-                                    }
-                                    fence_async_smem();
-                                    __syncwarp();
-                                    if (lane == 0) {
-                                        if (kOutEbuf<kOut> && store_y) tma_store_2d(&map_y, buf, n, row0, pol_y);
-                                        if constexpr (kOutQuant<kOut>)
-                                            tma_store_2d(&map_q, qbuf0 + (C::kQBufs == 2 ? eb : 0) * C::kQBuf,
-                                                         kOutE4M3<kOut> ? n : n / 2, row0,
-                                                         pol_y);
-                                        bulk_commit();
-                                    }
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    if (kOutEbuf<kOut> && store_y) tma_store_2d(&map_y, buf, n, row0, pol_y);
+                    if constexpr (kOutQuant<kOut>)
+                        tma_store_2d(&map_q, qb, kOutE4M3<kOut> ? n : n / 2, row0, pol_y);
+                    bulk_commit();
+                }
                 eb ^= 1;
                 return sc_byte;
             };

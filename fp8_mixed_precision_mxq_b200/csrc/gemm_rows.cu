@@ -82,6 +82,7 @@ struct Cfg {
 
 struct RowsParams {
     int M, N, K, k_stages;
+    int split;    // the cluster: one CTA per range of K
     int act;
     int out_fmt;  // MXQ_OUT_BF16, or the MX format of a gated h
     int gate_f32;
@@ -206,10 +207,10 @@ __global__ void __launch_bounds__(kThreads, 2)
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const int split = gridDim.x;  // the cluster: one CTA per range of K
-    const int rank = blockIdx.x;
-    const int tile = blockIdx.y;
-    const int m0 = blockIdx.z * kNT;       // the CTA's tokens
+    const int split = p.split;  // a power of two
+    const int rank = blockIdx.x & (split - 1);
+    const int tile = static_cast<int>(blockIdx.x) >> (31 - __clz(split));
+    const int m0 = blockIdx.y * kNT;  // the CTA's tokens
     const int M = min(kNT, p.M - m0);
     const int ks0 = static_cast<int>(static_cast<int64_t>(p.k_stages) * rank / split);
     const int ks1 = static_cast<int>(static_cast<int64_t>(p.k_stages) * (rank + 1) / split);
@@ -568,7 +569,7 @@ cudaError_t launch_rows(const CUtensorMap (&m)[3], const RowsParams& p, dim3 gri
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = grid.x;
+    attr[0].val.clusterDim.x = p.split;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -689,7 +690,8 @@ int launch_gemm_rows(const GemmArgs& g, cudaStream_t stream, const char** msg, c
     const int tiles = static_cast<int>(ceil_div(g.N, 128) * ceil_div(g.M, nt));
     int split = 1;
     while (split < kMaxSplit && 2 * split * tiles <= 2 * sms && 2 * split <= p.k_stages) split *= 2;
-    const dim3 grid(split, static_cast<unsigned>(ceil_div(g.N, 128)), static_cast<unsigned>(ceil_div(g.M, nt)));
+    p.split = split;
+    const dim3 grid(static_cast<unsigned>(split * ceil_div(g.N, 128)), static_cast<unsigned>(ceil_div(g.M, nt)), 1);
     cudaError_t e = kind == kBf16   ? launch_kind<kBf16>(gated, nt, m, p, grid, stream)
                     : kind == kMxf8 ? launch_kind<kMxf8>(gated, nt, m, p, grid, stream)
                                     : launch_kind<kMxf4>(gated, nt, m, p, grid, stream);

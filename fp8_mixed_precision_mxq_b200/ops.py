@@ -595,9 +595,14 @@ def _bf16_x(x, name) -> torch.device:
     return dev
 
 
-def _workspace(ws, need, dev):
+def _workspace(ws, need, dev, stream):
+    """The caller's workspace, or a new one that belongs to the stream its kernels run on (one of
+    another stream could be handed out again while they still use it)."""
     if ws is None:
-        return torch.empty(max(1, need), dtype=torch.uint8, device=dev)
+        if stream is None:
+            return torch.empty(max(1, need), dtype=torch.uint8, device=dev)
+        with torch.cuda.stream(stream):
+            return torch.empty(max(1, need), dtype=torch.uint8, device=dev)
     if ws.device != dev or not ws.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on %s" % dev)
     return ws
@@ -651,7 +656,8 @@ def linear_residual(x: torch.Tensor, w: QWeight, fmt="e2m1", act="none", residua
                     rows_per_group=None, workspace=None, out=None, stream=None):
     """linear() with gemm_residual's epilogue: x quantized on the fly to fmt, then
     y = residual + gate * act(x . deq(w)^T + bias).  workspace of
-    workspace_bytes(M, N, K, fmt) bytes; up to ROWS_QUANTIZED_IN_KERNEL rows need none."""
+    workspace_bytes(M, N, K, fmt) bytes; up to ROWS_QUANTIZED_IN_KERNEL rows need none.  out
+    must not overlap x (refused), also where x is the residual."""
     dev = _bf16_x(x, "x")
     M, K = x.shape
     f = _fmt(fmt)
@@ -661,7 +667,7 @@ def linear_residual(x: torch.Tensor, w: QWeight, fmt="e2m1", act="none", residua
     ws = wsb = 0
     if workspace is not None or M > ROWS_QUANTIZED_IN_KERNEL:
         nc, ns = _mx_bytes(M, K, f)
-        workspace = _workspace(workspace, (nc + 255) // 256 * 256 + (ns + 255) // 256 * 256, dev)
+        workspace = _workspace(workspace, (nc + 255) // 256 * 256 + (ns + 255) // 256 * 256, dev, stream)
         ws, wsb = workspace.data_ptr(), workspace.nbytes
     out = _bf16_out(out, M, w.N, dev)
     check(_lib.lib().mxq_linear_residual(x.data_ptr(), M, K, d.codes, d.sf, w.N, d.bias, f, e, ws, wsb,
@@ -713,7 +719,7 @@ def gated_ffn(x: torch.Tensor, gate: QWeight, up: QWeight, down: QWeight, act="s
     """The gated feed-forward network y = residual + out_gate * (quant(act(x . gate^T) *
     (x . up^T)) . down^T), biases included, with x quantized to up_fmt and the hidden
     activation kept quantized in down_fmt.  residual, out_gate and rows_per_group as
-    gemm_residual's residual, gate and rows_per_group; workspace of
+    gemm_residual's residual, gate and rows_per_group; out may be x; workspace of
     ffn_workspace_bytes(M, K, H, up_fmt, down_fmt) bytes."""
     dev = _bf16_x(x, "x")
     M, K = x.shape
@@ -721,7 +727,7 @@ def gated_ffn(x: torch.Tensor, gate: QWeight, up: QWeight, down: QWeight, act="s
     e = _epilogue("none", residual, out_gate, rows_per_group, M, down.N, dev)
     uf, df = _fmt(up_fmt), _fmt(down_fmt)
     need = sum((n + 255) // 256 * 256 for n in _mx_bytes(M, K, uf) + _mx_bytes(M, gate.N, df))
-    workspace = _workspace(workspace, need, dev)
+    workspace = _workspace(workspace, need, dev, stream)
     out = _bf16_out(out, M, down.N, dev)
     check(_lib.lib().mxq_gated_ffn(x.data_ptr(), M, K, dg, du, dd, _act(act), uf, df, e, workspace.data_ptr(),
                                    workspace.nbytes, out.data_ptr(),

@@ -470,7 +470,7 @@ int mxq_gemm_bf16_residual(const void* a_bf16, int64_t M, int64_t K, const void*
 /* mxq_linear (mode NATIVE) with that epilogue: x quantized to act_fmt into the workspace of
  * mxq_workspace_bytes(M, N, K, act_fmt, MXQ_MODE_NATIVE) bytes, then mxq_gemm_residual.  Up to
  * 16 rows are quantized inside the GEMM kernel, to the same codes; workspace is then not used
- * and may be NULL. */
+ * and may be NULL.  y must not overlap x (refused), also where x is the residual. */
 int mxq_linear_residual(const void* x_bf16, int64_t M, int64_t K, const void* w_codes, const void* w_sf, int64_t N,
                         const void* bias_bf16, int act_fmt, const mxq_epilogue* e, void* workspace, int64_t ws_bytes,
                         void* y_bf16, void* stream);
@@ -493,7 +493,7 @@ int mxq_gemm_bf16_gated(const void* a_bf16, int64_t M, int64_t K, const void* ga
 
 /* The gated feed-forward network: x quantized to up_fmt, mxq_gemm_gated with its h quantized
  * to down_fmt, then mxq_gemm_residual with the down weight and epilogue e (its act
- * MXQ_ACT_NONE).  x [M, K]; gate, up: N = H, K = K; down: K = H; y [M, down.N].  down_fmt E4M3
+ * MXQ_ACT_NONE).  x [M, K]; gate, up: N = H, K = K; down: K = H; y [M, down.N], which may be x.  down_fmt E4M3
  * needs H % 128 == 0.  workspace: mxq_ffn_workspace_bytes(M, K, H, up_fmt, down_fmt) bytes,
  * 256-byte aligned. */
 int mxq_gated_ffn(const void* x_bf16, int64_t M, int64_t K, const mxq_wdesc* gate, const mxq_wdesc* up,

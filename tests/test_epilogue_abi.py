@@ -57,6 +57,17 @@ def test_residual_gemms_check_their_operands():
                                  None) == _lib.ERR_ALIGN
 
 
+@pytest.mark.parametrize("M", [1, 16, 128])
+def test_linear_residual_refuses_an_output_over_its_input(M):
+    """Some of the few-row kernel's CTAs still read x while others write y, so no y may overlap it,
+    not even the x that is its own residual."""
+    L, e = _lib.lib(), epi()
+    far = 1 << 24
+    for x, y in ((far, far), (far, far + M * 256 * 2 - 16), (far, far - M * 512 * 2 + 16)):
+        got = L.mxq_linear_residual(x, M, 256, A16, A16, 512, None, 0, e, WS, 1 << 30, y, None)
+        assert got == _lib.ERR_INVALID_ARG and "overlaps" in _lib.last_error(), (x, y, _lib.last_error())
+
+
 def test_gated_gemms_check_their_operands():
     L = _lib.lib()
     w = _lib.WDesc(4096, 4096, None, 256, 512)

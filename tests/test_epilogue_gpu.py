@@ -351,6 +351,56 @@ def test_captured_replayed_and_on_two_streams(M):
     assert all(torch.equal(o, want) for o in outs) and ops.poll_status() == 0
 
 
+@pytest.mark.parametrize("M", [1, 16, 64, 300])
+def test_gated_ffn_adds_onto_its_own_input(M):
+    """The residual stream updated in place: x is the input, the residual and the output."""
+    ops = _ops()
+    g = gen(M + 7)
+    K, H = 512, 768
+    (wg, _), (wu, _), (wd, _) = weight(g, H, K), weight(g, H, K), weight(g, K, H)
+    x = normal(g, M, K)
+    want = ops.gated_ffn(x, wg, wu, wd, residual=x)
+    assert ops.gated_ffn(x, wg, wu, wd, residual=x, out=x) is x
+    assert torch.equal(x, want) and ops.poll_status() == 0
+
+
+@pytest.mark.parametrize("M", [64, 300])
+def test_a_call_on_another_stream_keeps_its_workspace(M):
+    """The workspace that a call allocates belongs to the stream it runs on: what the current stream
+    allocates and writes right behind it is other memory."""
+    ops = _ops()
+    g = gen(M + 9)
+    K, H = 512, 768
+    (wg, _), (wu, _), (wd, _) = weight(g, H, K), weight(g, H, K), weight(g, K, H)
+    w, x = weight(g, H, K)[0], normal(g, M, K)
+    want_y, want_f = ops.linear_residual(x, w), ops.gated_ffn(x, wg, wu, wd)
+    s = torch.cuda.Stream()
+    y, f = torch.empty_like(want_y), torch.empty_like(want_f)
+    torch.cuda.synchronize()
+    sizes = (ops.workspace_bytes(M, H, K, "e2m1"), ops.ffn_workspace_bytes(M, K, H, "e2m1", "e2m1"))
+    for _ in range(20):
+        ops.linear_residual(x, w, out=y, stream=s)
+        junk = [torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda") for n in sizes]
+        ops.gated_ffn(x, wg, wu, wd, out=f, stream=s)
+        junk += [torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda") for n in sizes]
+        del junk
+    torch.cuda.synchronize()
+    assert torch.equal(y, want_y) and torch.equal(f, want_f) and ops.poll_status() == 0
+
+
+def test_more_outputs_than_two_grid_dimensions_hold():
+    """One token over 65536 weight tiles of 128 outputs."""
+    ops = _ops()
+    g = gen(3)
+    N, K = 65536 * 128 + 8, 32
+    block = torch.randn((128, K), generator=g, device="cuda").bfloat16()
+    w = block.repeat(65537, 1)[:N].contiguous()
+    x = torch.randn((1, K), generator=g, device="cuda").bfloat16()
+    y = ops.gemm_bf16_residual(x, w, act="silu")
+    want = ops.gemm_bf16_residual(x, block, act="silu")
+    assert torch.equal(y, want.repeat(1, 65537)[:, :N]) and ops.poll_status() == 0
+
+
 @pytest.mark.parametrize("M", [8, 300, 5000])
 def test_a_wait_that_runs_out_is_reported(M):
     """Debug bit 0: a stage is never filled; the kernel's wait ends after its limit, the status
