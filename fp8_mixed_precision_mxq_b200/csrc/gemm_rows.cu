@@ -292,38 +292,36 @@ __global__ void __launch_bounds__(kThreads, 2)
     // Tokens are finished in fours: four a by rank a % split, its warps 0-3 and 4-7 taking
     // alternate ones of the rank's.  first4: this warp's first four.
     const int first4 = rank + split * (warp >> 2);
-    float b0 = 0.0f, b1 = 0.0f, gate4[4], res4[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        gate4[i] = 1.0f;
-        res4[i] = 0.0f;
-    }
+    // As loaded, so that nothing waits for the loads before the last step: bf16 bits in the low
+    // half, or a gate's fp32 bits.
+    uint32_t bias_r[2] = {0u, 0u}, gate_r[4], res_r[4];
     // gate and residual of a four of tokens
     auto load_four = [&](int a) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int t = 4 * a + i;
+            gate_r[i] = res_r[i] = 0u;
             if (kGated || !live || t >= M) continue;
             if (p.gate != nullptr) {
                 const size_t gi = static_cast<size_t>(static_cast<uint32_t>(m0 + t) / p.rows_per_group) * p.N + n;
-                gate4[i] = p.gate_f32 ? __ldg(static_cast<const float*>(p.gate) + gi)
-                                      : __bfloat162float(static_cast<const __nv_bfloat16*>(p.gate)[gi]);
+                gate_r[i] = p.gate_f32 ? __ldg(static_cast<const uint32_t*>(p.gate) + gi)
+                                       : __ldg(static_cast<const uint16_t*>(p.gate) + gi);
             }
-            if (p.res != nullptr) res4[i] = __bfloat162float(p.res[static_cast<size_t>(m0 + t) * p.N + n]);
+            if (p.res != nullptr)
+                res_r[i] = reinterpret_cast<const uint16_t*>(p.res)[static_cast<size_t>(m0 + t) * p.N + n];
         }
     };
     // what the last step needs from memory, fetched while the weight streams
     auto load_epilogue = [&]() {
-        if (!live || 4 * first4 >= M) return;
-        if (p.bias != nullptr) b0 = __bfloat162float(p.bias[n]);
-        if (kGated && p.bias2 != nullptr) b1 = __bfloat162float(p.bias2[n]);
         load_four(first4);
+        if (!live || 4 * first4 >= M) return;
+        if (p.bias != nullptr) bias_r[0] = __ldg(reinterpret_cast<const uint16_t*>(p.bias) + n);
+        if (kGated && p.bias2 != nullptr) bias_r[1] = __ldg(reinterpret_cast<const uint16_t*>(p.bias2) + n);
     };
 
     if (warp == 0) {
+        grid_wait();
         if (lane == 0) {
-            bool ok = true;
-            if (p.early) grid_wait();
             grid_launch_dependents();  // after the wait: see the head of the file
             if constexpr (!kQX) {
                 for (int it = 0; it < n_first; ++it) {
@@ -332,6 +330,11 @@ __global__ void __launch_bounds__(kThreads, 2)
                     if constexpr (kKind != kBf16) load_sf(C::kW, it);
                 }
             }
+        }
+        __syncwarp();
+        load_epilogue();
+        if (lane == 0) {
+            bool ok = true;
             int it = n_first;
             for (; it < n_stages; ++it) {
                 if (!mbar_wait(&empty[it % S], ((it / S) & 1) ^ 1, kWaitNs)) {
@@ -354,6 +357,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         __syncwarp();
     } else if (warp == 1) {
+        grid_wait();
+        load_epilogue();
         if (lane == 0) {
             constexpr uint32_t fw = kKind == kMxf8 ? 5u : 1u;  // weight: E2M1 in both kinds
             constexpr uint32_t fx = kKind == kMxf8 ? 0u : 1u;  // activation: E4M3 / E2M1
@@ -479,75 +484,100 @@ __global__ void __launch_bounds__(kThreads, 2)
     tc_fence_after();
     if (warp == 1) tmem_dealloc<1>(tmem, C::kTmem);
 
-    uint32_t bad = 0u;
+    uint32_t bad = 0u;  // first used at the stores: the first partials are on their way before it is here
 #pragma unroll
     for (int r = 0; r < kMaxSplit; ++r)
         if (r < split) bad |= ld_cluster_u32(mapa_shared(smem_u32(failed), r));
     const int fours = (M + 3) / 4;
-    if (warp < 2) {  // these two had other work until now
-        grid_wait();
-        load_epilogue();
-    }
-    if (bad != 0u || first4 >= fours) cluster_arrive();  // nothing (more) to read from the peers
-    if (bad == 0u)
-        with_act(p.act, [&](auto act) {
-            for (int a = first4; a < fours; a += split * 2) {
-                float4 v[C::kW];
+    if (first4 >= fours) cluster_arrive();  // nothing to read from the peers
+    with_act(p.act, [&](auto act) {
+#pragma unroll 1
+        for (int a = first4; a < fours; a += split * 2) {
+            float4 v[C::kW];
 #pragma unroll
-                for (int w = 0; w < C::kW; ++w) {
-                    const uint32_t at = smem_u32(part + (w * (kNT / 4) + a) * 128 + (warp & 3) * 32 + lane);
-                    float4 f[kMaxSplit];
+            for (int w = 0; w < C::kW; ++w) {
+                const uint32_t at = smem_u32(part + (w * (kNT / 4) + a) * 128 + (warp & 3) * 32 + lane);
+                float4 f[kMaxSplit];
 #pragma unroll
-                    for (int r = 0; r < kMaxSplit; ++r)
-                        f[r] = r < split ? ld_cluster_f32x4(mapa_shared(at, r)) : make_float4(0.f, 0.f, 0.f, 0.f);
-                    v[w] = f[0];
+                for (int r = 0; r < kMaxSplit; ++r)
+                    f[r] = r < split ? ld_cluster_f32x4(mapa_shared(at, r)) : make_float4(0.f, 0.f, 0.f, 0.f);
+                v[w] = f[0];
 #pragma unroll
-                    for (int r = 1; r < kMaxSplit; ++r) {
-                        v[w].x += f[r].x;
-                        v[w].y += f[r].y;
-                        v[w].z += f[r].z;
-                        v[w].w += f[r].w;
-                    }
-                }
-                // the peers may leave once the last four has been read; what follows is local
-                if (a + split * 2 >= fours) cluster_arrive();
-                if (a != first4) load_four(a);
-                const float s0[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
-                [[maybe_unused]] const float s1[4] = {v[C::kW - 1].x, v[C::kW - 1].y, v[C::kW - 1].z, v[C::kW - 1].w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int t = 4 * a + i;
-                    if (t >= M) break;
-                    float o = act_f32<act>(s0[i] + b0);
-                    if constexpr (kGated) o *= s1[i] + b1;
-                    else o = fmaf(o, gate4[i], res4[i]);
-                    if (!kGated || p.out_fmt == MXQ_OUT_BF16) {
-                        if (live) p.y[static_cast<size_t>(m0 + t) * p.N + n] = __float2bfloat16_rn(o);
-                        continue;
-                    }
-                    // h: the warp's 32 values of this token are one MX block (N is a multiple of 32)
-                    uint32_t sc = 0u;
-                    if (nq < p.N) {
-                        const uint32_t hb = bf16x2_bits(o, o);
-                        const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, hb & 0x7FFFu);
-                        const bool e4m3 = p.out_fmt == MXQ_FMT_E4M3;
-                        sc = e4m3 ? e8m0_code<8u>(m) : e8m0_code<2u>(m);
-                        const float q = lo_f(hb) * e8m0_inverse(sc);
-                        const float q1 = __shfl_down_sync(0xFFFFFFFFu, q, 1);
-                        if (e4m3) {
-                            p.q_codes[static_cast<size_t>(m0 + t) * p.N + n] =
-                                sc == 255u ? uint8_t(0) : static_cast<uint8_t>(cvt_e4m3x2(q, 0.0f) & 0xFFu);
-                        } else if ((lane & 1) == 0) {
-                            const float pair[8] = {q, q1, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                            p.q_codes[(static_cast<size_t>(m0 + t) * p.N + n) / 2] =
-                                sc == 255u ? uint8_t(0) : static_cast<uint8_t>(cvt_e2m1x8(pair) & 0xFFu);
-                        }
-                    }
-                    if (lane == 0)  // this token's scale byte (0 for the padding past N)
-                        p.q_sf[sf_word(m0 + t, tile, p.atoms_n) + (warp & 3)] = static_cast<uint8_t>(sc);
+                for (int r = 1; r < kMaxSplit; ++r) {
+                    v[w].x += f[r].x;
+                    v[w].y += f[r].y;
+                    v[w].z += f[r].z;
+                    v[w].w += f[r].w;
                 }
             }
-        });
+            // the peers may leave once the last four has been read; what follows is local
+            if (a + split * 2 >= fours) cluster_arrive();
+            // four tokens side by side: each step's latency is paid once for all of them
+            float o[4];
+            const float b0 = __uint_as_float(bias_r[0] << 16);
+            const float2 lo = act_f32x2<act>(__fadd2_rn(make_float2(v[0].x, v[0].y), make_float2(b0, b0)));
+            const float2 hi = act_f32x2<act>(__fadd2_rn(make_float2(v[0].z, v[0].w), make_float2(b0, b0)));
+            if constexpr (kGated) {
+                const float b1 = __uint_as_float(bias_r[1] << 16);
+                constexpr int u = C::kW - 1;
+                o[0] = lo.x * (v[u].x + b1);
+                o[1] = lo.y * (v[u].y + b1);
+                o[2] = hi.x * (v[u].z + b1);
+                o[3] = hi.y * (v[u].w + b1);
+            } else {
+                const float q[4] = {lo.x, lo.y, hi.x, hi.y};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float g = p.gate == nullptr ? 1.0f : __uint_as_float(p.gate_f32 ? gate_r[i] : gate_r[i] << 16);
+                    o[i] = fmaf(q[i], g, __uint_as_float(res_r[i] << 16));
+                }
+                if (a + split * 2 < fours) load_four(a + split * 2);
+            }
+            const int n_live = bad != 0u ? 0 : min(4, M - 4 * a);  // a cluster that timed out writes nothing
+            const size_t row = static_cast<size_t>(m0 + 4 * a);
+            if (!kGated || p.out_fmt == MXQ_OUT_BF16) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (live && i < n_live) p.y[(row + i) * p.N + n] = __float2bfloat16_rn(o[i]);
+                continue;
+            }
+            if constexpr (kGated) {
+                // h: the warp's 32 values of a token are one MX block (N is a multiple of 32); past N
+                // they are the scale layout's padding, zeros
+                const bool e4m3 = p.out_fmt == MXQ_FMT_E4M3, in = nq < p.N;
+                uint32_t m[4], sc[4], code[4];
+                float q[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) m[i] = bf16x2_bits(o[i], o[i]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, m[i] & 0x7FFFu);
+                    sc[i] = e4m3 ? e8m0_code<8u>(top) : e8m0_code<2u>(top);
+                    q[i] = lo_f(m[i]) * e8m0_inverse(sc[i]);
+                }
+                if (e4m3) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        code[i] = sc[i] == 255u ? 0u : cvt_e4m3x2(q[i], 0.0f);
+                        if (in && i < n_live) p.q_codes[(row + i) * p.N + n] = static_cast<uint8_t>(code[i]);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float pair[8] = {q[i], __shfl_down_sync(0xFFFFFFFFu, q[i], 1), 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                        code[i] = sc[i] == 255u ? 0u : cvt_e2m1x8(pair);
+                        if (in && i < n_live && (lane & 1) == 0)
+                            p.q_codes[((row + i) * p.N + n) / 2] = static_cast<uint8_t>(code[i]);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (lane == 0 && i < n_live)
+                        p.q_sf[sf_word(m0 + 4 * a + i, tile, p.atoms_n) + (warp & 3)] =
+                            in ? static_cast<uint8_t>(sc[i]) : uint8_t(0);
+            }
+        }
+    });
     // the layout's padding rows, one word of this tile each
     if (kGated && p.out_fmt != MXQ_OUT_BF16 && rank == 0 && bad == 0u && m0 + kNT >= p.M)
         for (int t = p.M + static_cast<int>(threadIdx.x); t < (p.M + 127) / 128 * 128; t += kThreads)
