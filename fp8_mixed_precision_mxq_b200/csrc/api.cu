@@ -338,10 +338,11 @@ void set_gated(GemmArgs& g, const void* w2, const void* w2_sf, const void* bias2
 
 int run_gemm_gated(const void* a_codes, const void* a_sf, int a_fmt, int64_t M, int64_t K, const mxq_wdesc& gate,
                    const mxq_wdesc& up, int act, int out_fmt, void* out, void* out_sf, cudaStream_t stream,
-                   const void* x = nullptr)
+                   const void* x = nullptr, bool early = false)
 {
     GemmArgs g{a_codes, a_sf, a_fmt, M, gate.N, K, gate.codes, gate.sf, gate.bias, nullptr};
     g.x = x;
+    g.early = early;
     set_gated(g, up.codes, up.sf, up.bias, act, out_fmt, out, out_sf);
     return run_epilogue_gemm(g, "gated gemm", stream);
 }
@@ -1047,7 +1048,7 @@ int mxq_linear_residual(const void* x_bf16, int64_t M, int64_t K, const void* w_
     uint8_t* xc = static_cast<uint8_t*>(workspace);
     uint8_t* xs = xc + round_up(codes_bytes(M, K, act_fmt), kWsAlign);
     RETURN_IF(cuda_rc(launch_quantize(x_bf16, M, K, act_fmt, xc, xs, st), "quantize launch"));
-    return run_gemm_residual(xc, xs, act_fmt, M, K, w_codes, w_sf, N, bias_bf16, *e, y_bf16, st);
+    return run_gemm_residual(xc, xs, act_fmt, M, K, w_codes, w_sf, N, bias_bf16, *e, y_bf16, st, nullptr, true);
 }
 
 int mxq_gemm_gated(const void* a_codes, const void* a_sf, int a_fmt, int64_t M, int64_t K, const mxq_wdesc* gate,
@@ -1111,11 +1112,12 @@ int mxq_gated_ffn(const void* x_bf16, int64_t M, int64_t K, const mxq_wdesc* gat
     uint8_t* hs = hc + round_up(codes_bytes(M, H, down_fmt), kWsAlign);
     const bool fused = M <= kRowsMaxQuantM;  // x is quantized inside the first kernel
     if (!fused) RETURN_IF(cuda_rc(launch_quantize(x_bf16, M, K, up_fmt, xc, xs, st), "quantize launch"));
-    RETURN_IF(run_gemm_gated(xc, xs, up_fmt, M, K, *gate, *up, act, down_fmt, hc, hs, st, fused ? x_bf16 : nullptr));
+    RETURN_IF(run_gemm_gated(xc, xs, up_fmt, M, K, *gate, *up, act, down_fmt, hc, hs, st, fused ? x_bf16 : nullptr,
+                             !fused));
     char gp[sizeof g_path];
     snprintf(gp, sizeof gp, "%s", g_path);
     RETURN_IF(run_gemm_residual(hc, hs, down_fmt, M, H, down->codes, down->sf, down->N, down->bias, *e, y_bf16, st,
-                                nullptr, M <= kRowsTileM));
+                                nullptr, true));
     char dp[sizeof g_path];
     snprintf(dp, sizeof dp, "%s", g_path);
     snprintf(g_path, sizeof g_path, "gated ffn: %.110s | %.110s", gp, dp);

@@ -19,9 +19,11 @@
 // timing), and apply bias, activation, gate and residual, or the gated product and the MX
 // quantization (32 lanes = 32 consecutive outputs = one MX block).
 // Launches are programmatic: the set-up runs while the kernel before on the stream ends.  All
-// global reads and writes come after griddepcontrol.wait, except that the second kernel of the
-// gated network starts on its weight before it (the first kernel allows that only after its own
-// wait, so whatever wrote the weight has long completed).
+// global reads and writes come after griddepcontrol.wait, except that behind a kernel of the same
+// call (the quantizer of x, or the gated network's first kernel) the weight is read before it: the
+// quantizer is an ordinary launch and the first kernel lets this one start only after its own wait,
+// so whatever wrote the weight has completed.  (48 rows of 5120 x 13824 W4A8, quantizer included:
+// 19.2 us, 20.3 without.)
 // Every wait is bounded; one that runs out records MXQ_ERR_TIMEOUT, the copies in flight are
 // waited for, TMEM is freed and no output is written.
 #include <cuda_bf16.h>
@@ -122,9 +124,6 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr)
                  : "memory");
     return v;
 }
-
-__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // Quantizes rows x[0 .. M) of one stage (kKps columns from k0) into the stage's operand tile
 // (128-byte rows under the 128-byte swizzle) and scale atoms, with the activation quantizer's

@@ -99,9 +99,9 @@ struct GemmArgs {
     const void* w2_codes = nullptr;
     const void* w2_sf = nullptr;
     const void* bias2 = nullptr;
-    // few-row kernel only (M <= kRowsTileM).  x: the activation in bf16 (M <= kRowsMaxQuantM), quantized to a_fmt
-    // inside the kernel; a_codes and a_sf are not read.  early: the kernel before on the stream
-    // is this library's, launched behind everything that wrote the weight.
+    // few-row kernel only.  x: the activation in bf16 (M <= kRowsMaxQuantM), quantized to a_fmt
+    // inside the kernel; a_codes and a_sf are not read.  early: the kernel before on the stream is
+    // of the same call, and starts behind everything that wrote the weight.
     const void* x = nullptr;
     bool early = false;
 };

@@ -21,6 +21,7 @@
 
 #include "mx_elem.cuh"
 #include "mxq_internal.h"
+#include "ptx.cuh"
 
 namespace mxq {
 
@@ -404,6 +405,7 @@ template <bool kF32, bool kVF32, bool kQuant, int C, int R, bool kFull, bool kEa
 __global__ void __maxnreg__(norm_regs(kF32, C, R, kEarly)) norm_residual_kernel(const NormParams p)
 {
     __shared__ float red[4 * R * kMaxWarps];
+    grid_launch_dependents();  // a few-row GEMM behind it sets up meanwhile
     const uint32_t lane = threadIdx.x & 31u;
     const uint32_t per_group = (p.rows_per_group + R - 1) / R;  // CTAs a group
     const uint32_t group = blockIdx.x / per_group;

@@ -128,6 +128,7 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const uint4* __restr
     const uint32_t lane = threadIdx.x & 31u;
     const uint32_t nwarps = gridDim.x * (kThreads / 32);
     const uint32_t warp = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    grid_launch_dependents();  // a few-row GEMM behind it sets up, and reads its weight, meanwhile
 
     static_assert(kUnroll % 4 == 0, "the scale bytes of a step are stored kUnroll / 4 per lane");
     for (uint32_t w0 = warp; w0 * 32u < n_groups; w0 += nwarps * kUnroll) {
