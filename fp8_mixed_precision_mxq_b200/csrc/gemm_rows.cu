@@ -23,13 +23,14 @@
 // call (the quantizer of x, or the gated network's first kernel) the weight is read before it: the
 // quantizer is an ordinary launch and the first kernel lets this one start only after its own wait,
 // so whatever wrote the weight has completed.  (48 rows of 5120 x 13824 W4A8, quantizer included:
-// 19.2 us, 20.3 without.)
+// 19.2 us with K split in 4, 20.3 without.)
 // Every wait is bounded; one that runs out records MXQ_ERR_TIMEOUT, the copies in flight are
 // waited for, TMEM is freed and no output is written.
 #include <cuda_bf16.h>
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstdio>
 
 #include "mx_elem.cuh"
@@ -84,7 +85,7 @@ struct Cfg {
 
 struct RowsParams {
     int M, N, K, k_stages;
-    int split;    // the cluster: one CTA per range of K
+    int split;  // the cluster: one CTA per range of K
     int act;
     int out_fmt;  // MXQ_OUT_BF16, or the MX format of a gated h
     int gate_f32;
@@ -206,9 +207,9 @@ __global__ void __launch_bounds__(kThreads, 2)
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const int split = p.split;  // a power of two
-    const int rank = blockIdx.x & (split - 1);
-    const int tile = static_cast<int>(blockIdx.x) >> (31 - __clz(split));
+    const int split = p.split;
+    const int rank = static_cast<int>(cluster_ctarank());
+    const int tile = static_cast<int>(cluster_id_x());
     const int m0 = blockIdx.y * kNT;  // the CTA's tokens
     const int M = min(kNT, p.M - m0);
     const int ks0 = static_cast<int>(static_cast<int64_t>(p.k_stages) * rank / split);
@@ -584,18 +585,80 @@ __global__ void __launch_bounds__(kThreads, 2)
     cluster_wait();  // no CTA leaves while another may read its partials
 }
 
+// The footprint of a few-row CTA of which one or two fit an SM, without its tensor memory: for a kernel
+// that allocates it the runtime counts one CTA an SM, though here each takes at most half of it.
+__global__ void __launch_bounds__(kThreads, 2) footprint_kernel() {}
+
+// How many clusters of that many CTAs the current device holds at once, one or two CTAs an SM.  A
+// property of the device (of its GPCs' sizes), asked for once.
+int clusters_at_once(int split, int per_sm)
+{
+    constexpr int kDevices = 64;
+    static std::atomic<int> known[kDevices][2][kMaxSplit + 1];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    if (dev < kDevices)
+        if (const int n = known[dev][per_sm - 1][split].load(std::memory_order_relaxed)) return n;
+    const int smem = per_sm == 1 ? 227 * 1024 : 113 * 1024;
+    if (cudaFuncSetAttribute(footprint_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) != cudaSuccess)
+        return 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(split, 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = split;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, footprint_kernel, &cfg) != cudaSuccess) return 0;
+    if (dev < kDevices) known[dev][per_sm - 1][split].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+// The ways K is split over a cluster.  All clusters run at once (148 SMs hold 71 of four CTAs, 45 of
+// six, 37 of seven, 33 of eight; a second wave costs the whole time again: 40 tiles of 5120 x 13824
+// W4A8, 48 rows, in 7 ranges 22.9 us, in 6 14.4).  A range's stages then take the longer of their round
+// trip over the ring's depth and their share of the memory's rate, and CTAs that share an SM
+// delay each other's set-up and last step by about 0.9 us for 16 tokens.  Measured against the
+// widest split that fits: 40 tiles of K = 5120 W4A4, 48 rows, gated, in 3 11.5 us, in 6 13.4; 48
+// tiles of K = 4096, one row, in 2 7.2, in 5 7.6.
+int split_for(int k_stages, int64_t tiles_n, int64_t tiles_m, int stage_bytes, int ring, int nt)
+{
+    constexpr double kRoundTripUs = 2.0, kBytesPerUs = 6.4e6, kSharedUs = 0.9 / 16;
+    const int64_t tiles = tiles_n * tiles_m;
+    int best = 1;
+    double best_us = 0.0;
+    for (int split = 1; split <= std::min(kMaxSplit, k_stages); ++split) {
+        const bool alone = tiles <= clusters_at_once(split, 1);
+        if (split > 1 && !alone && tiles > clusters_at_once(split, 2)) continue;
+        const double stage = std::max(kRoundTripUs / ring, static_cast<double>(tiles_n) * split * stage_bytes / kBytesPerUs);
+        const double us = static_cast<double>(ceil_div(k_stages, split)) * stage + (alone ? 0.0 : kSharedUs * nt);
+        if (split == 1 || us < best_us) {
+            best = split;
+            best_us = us;
+        }
+    }
+    return best;
+}
+
 template <int kKind, bool kGated, int kNT, bool kQX>
-cudaError_t launch_rows(const CUtensorMap (&m)[3], const RowsParams& p, dim3 grid, cudaStream_t stream)
+cudaError_t launch_rows(const CUtensorMap (&m)[3], RowsParams& p, cudaStream_t stream)
 {
     using C = Cfg<kKind, kGated, kNT>;
+    const int64_t tiles_n = ceil_div(p.N, 128), tiles_m = ceil_div(p.M, kNT);
+    p.split = split_for(p.k_stages, tiles_n, tiles_m, C::kTxW + C::kW * C::kSf, C::kStages, kNT);
     auto kern = gemm_rows_kernel<kKind, kGated, kNT, kQX>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
     cfg.blockDim = dim3(kThreads, 1, 1);
     cfg.dynamicSmemBytes = C::kSmem;
     cfg.stream = stream;
+    cfg.gridDim = dim3(static_cast<unsigned>(p.split * tiles_n), static_cast<unsigned>(tiles_m), 1);
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = p.split;
@@ -609,22 +672,20 @@ cudaError_t launch_rows(const CUtensorMap (&m)[3], const RowsParams& p, dim3 gri
 }
 
 template <int kKind, bool kGated>
-cudaError_t launch_nt(int nt, const CUtensorMap (&m)[3], const RowsParams& p, dim3 grid,
-                      cudaStream_t stream)
+cudaError_t launch_nt(int nt, const CUtensorMap (&m)[3], RowsParams& p, cudaStream_t stream)
 {
     if constexpr (kKind != kBf16)
-        if (p.x != nullptr) return launch_rows<kKind, kGated, 16, true>(m, p, grid, stream);
-    if (nt == 16) return launch_rows<kKind, kGated, 16, false>(m, p, grid, stream);
-    if (nt == 32) return launch_rows<kKind, kGated, 32, false>(m, p, grid, stream);
-    return launch_rows<kKind, kGated, 64, false>(m, p, grid, stream);
+        if (p.x != nullptr) return launch_rows<kKind, kGated, 16, true>(m, p, stream);
+    if (nt == 16) return launch_rows<kKind, kGated, 16, false>(m, p, stream);
+    if (nt == 32) return launch_rows<kKind, kGated, 32, false>(m, p, stream);
+    return launch_rows<kKind, kGated, 64, false>(m, p, stream);
 }
 
 template <int kKind>
-cudaError_t launch_kind(bool gated, int nt, const CUtensorMap (&m)[3], const RowsParams& p, dim3 grid,
-                        cudaStream_t stream)
+cudaError_t launch_kind(bool gated, int nt, const CUtensorMap (&m)[3], RowsParams& p, cudaStream_t stream)
 {
-    return gated ? launch_nt<kKind, true>(nt, m, p, grid, stream)
-                 : launch_nt<kKind, false>(nt, m, p, grid, stream);
+    return gated ? launch_nt<kKind, true>(nt, m, p, stream)
+                 : launch_nt<kKind, false>(nt, m, p, stream);
 }
 
 }  // namespace
@@ -654,7 +715,8 @@ bool few_rows(const GemmArgs& g)
 {
     if (g.M <= kRowsTileM) return true;
     const int64_t tiles = ceil_div(g.M, kRowsTileM) * ceil_div(g.N, 128);
-    return tiles * (g.epilogue == kEpilogueGated ? 2 : 1) <= num_sms();
+    const bool w4a8 = !g.bf16 && g.a_fmt == kFmtE4M3;
+    return tiles * (g.epilogue == kEpilogueGated ? 2 : 1) <= num_sms() * (w4a8 ? 2 : 1);
 }
 
 int launch_gemm_rows(const GemmArgs& g, cudaStream_t stream, const char** msg, char* path, size_t path_len)
@@ -714,16 +776,9 @@ int launch_gemm_rows(const GemmArgs& g, cudaStream_t stream, const char** msg, c
     p.q_codes = static_cast<uint8_t*>(g.q_codes);
     p.q_sf = static_cast<uint8_t*>(g.q_sf);
 
-    // K is split while all CTAs still run at once, two to an SM
-    const int sms = num_sms();
-    const int tiles = static_cast<int>(ceil_div(g.N, 128) * ceil_div(g.M, nt));
-    int split = 1;
-    while (split < kMaxSplit && 2 * split * tiles <= 2 * sms && 2 * split <= p.k_stages) split *= 2;
-    p.split = split;
-    const dim3 grid(static_cast<unsigned>(split * ceil_div(g.N, 128)), static_cast<unsigned>(ceil_div(g.M, nt)), 1);
-    cudaError_t e = kind == kBf16   ? launch_kind<kBf16>(gated, nt, m, p, grid, stream)
-                    : kind == kMxf8 ? launch_kind<kMxf8>(gated, nt, m, p, grid, stream)
-                                    : launch_kind<kMxf4>(gated, nt, m, p, grid, stream);
+    cudaError_t e = kind == kBf16   ? launch_kind<kBf16>(gated, nt, m, p, stream)
+                    : kind == kMxf8 ? launch_kind<kMxf8>(gated, nt, m, p, stream)
+                                    : launch_kind<kMxf4>(gated, nt, m, p, stream);
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) {
         *msg = cudaGetErrorString(e);
@@ -731,7 +786,7 @@ int launch_gemm_rows(const GemmArgs& g, cudaStream_t stream, const char** msg, c
     }
     if (path)
         snprintf(path, path_len, "rows%s %s 128x%d split %d tiles %d%s", g.x ? " +quantize x" : "", kind == kBf16 ? "bf16" : kind == kMxf8 ? "mxf8f6f4" : "mxf4",
-                 nt, split, tiles, epilogue_name(g));
+                 nt, p.split, static_cast<int>(ceil_div(g.N, 128) * ceil_div(g.M, nt)), epilogue_name(g));
     return MXQ_OK;
 }
 

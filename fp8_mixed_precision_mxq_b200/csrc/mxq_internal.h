@@ -114,11 +114,13 @@ const char* epilogue_name(const GemmArgs& g);  // for the path description
 
 // The residual or gated GEMM for few activation rows (gemm_rows.cu); arguments and results as
 // launch_gemm's.  It takes up to kRowsTileM rows of any output, and more where the output has no
-// more 128 x kRowsTileM tiles (counting both weights of a gated pair) than the GPU has SMs: one
-// wave of them ends before the pair kernel's 256 x 256 tiles, which leave most SMs idle there.
-// Measured (us, this kernel / the pair kernel): W4A4 residual 5120 x 5120 at 192 rows (120 tiles)
-// 11.7 / 17.0, at 256 (160) 17.6 / 17.2; W4A8 K = 13824 at 192 rows 27 / 53; gated 5120 x 5120
-// W4A4 at 64 rows (80) 12.7 / 15.9, at 128 (160) 16.8 / 15.9; 1024 x 1024 at 1024 rows (128) 7.9 / 10.6.
+// more 128 x kRowsTileM tiles (counting both weights of a gated pair) than the GPU has SMs, for W4A8
+// twice as many: one wave of them ends before the pair kernel's 256 x 256 tiles, which leave most
+// SMs idle there.  Measured (us, this kernel / the pair kernel, residual unless said): 5120 x 5120
+// W4A4 at 192 rows (120 tiles) 13.2 / 18.9, at 320 (200) 20.1 / 19.5; 5120 x 4096 bf16 at 192 20.5 /
+// 28.8, at 256 (160) 33.2 / 29.0; 5120 x 13824 W4A8 at 192 27.8 / 54.5, at 448 (280) 51.4 / 55.2; gated
+// W4A8 2560 x 8192 at 128 (80) 18.9 / 33.7, at 256 (160) 24.7 / 34.1; gated 5120 x 5120 W4A4 at 64 (80)
+// 12.4 / 16.5, at 192 (240) 17.7 / 16.6.
 constexpr int64_t kRowsTileM = 64;
 bool few_rows(const GemmArgs& g);
 constexpr int64_t kRowsMaxQuantM = 16;

@@ -137,6 +137,13 @@ __device__ __forceinline__ uint64_t policy_evict_normal()
 // ---------------------------------------------------------------------------
 // clusters
 // ---------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t cluster_id_x()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%clusterid.x;" : "=r"(r));
+    return r;
+}
+
 __device__ __forceinline__ uint32_t cluster_ctarank()
 {
     uint32_t r;

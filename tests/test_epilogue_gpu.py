@@ -106,10 +106,11 @@ def weight(g, N, K, bias=True, std=0.05):
     return q, deq(q.codes, q.sf, N, K, "e2m1")
 
 
-def on_few_rows(M, N, gated=False):
-    """The library's choice of kernel: few rows, or an output of at most an SM count of tiles."""
+def on_few_rows(M, N, fmt, gated=False):
+    """The library's choice of kernel: few rows, or an output of at most an SM count of tiles (W4A8:
+    two)."""
     sms = torch.cuda.get_device_properties(0).multi_processor_count
-    return M <= 64 or -(-M // 64) * -(-N // 128) * (2 if gated else 1) <= sms
+    return M <= 64 or -(-M // 64) * -(-N // 128) * (2 if gated else 1) <= sms * (2 if fmt == "e4m3" else 1)
 
 
 # The few-row kernel's widths and both sides of its borders (16, 32 and 64 tokens; several token
@@ -130,8 +131,10 @@ RESIDUAL = [  # M, N, K, fmt, act, bias, residual, gate groups, gate dtype
     (1000, 264, 544, "e2m1", "none", True, True, 7, torch.float32),
     (65, 9608, 32, "e2m1", "none", False, True, 0, None),
     (129, 6408, 256, "e4m3", "gelu", True, True, 3, torch.bfloat16),   # groups that end inside a warp's rows
+    (129, 12808, 256, "e4m3", "gelu", True, True, 3, torch.bfloat16),   # groups that end inside a warp's rows
     (300, 4104, 1024, "e2m1", "gelu_tanh", True, False, 0, None),
     (513, 2200, 2048, "e4m3", "silu", True, True, 513, torch.float32),  # a group for each row
+    (700, 4104, 384, "e4m3", "silu", True, True, 513, torch.float32),  # a group for each row
     (1000, 5120, 1280, "e2m1", "none", True, True, 2, torch.float32),
 ]
 
@@ -147,7 +150,7 @@ def test_gemm_residual_against_float64(M, N, K, fmt, act, bias, residual, groups
     rpg = -(-M // max(1, groups))
     y = ops.gemm_residual(*a, w, act=act, residual=r, gate=gate, rows_per_group=rpg)
     assert ops.poll_status() == 0
-    assert ops.last_path().startswith("rows") == on_few_rows(M, N) and "+act+residual" in ops.last_path()
+    assert ops.last_path().startswith("rows") == on_few_rows(M, N, fmt) and "+act+residual" in ops.last_path()
     check_residual(y, a64, w64, w.bias, act, r, gate, rpg, "M=%d N=%d K=%d %s %s" % (M, N, K, fmt, act))
     # in place of the residual: the same bits
     if residual:
@@ -210,6 +213,7 @@ GATED = [  # M, H, K, fmt, act, bias
     (65, 4768, 544, "e2m1", "gelu", True),
     (300, 2080, 32, "e2m1", "gelu", True),
     (257, 2088, 512, "e4m3", "gelu_tanh", True),
+    (300, 4104, 384, "e4m3", "gelu_tanh", True),
     (777, 5632, 2048, "e4m3", "silu", True),
 ]
 
@@ -222,7 +226,7 @@ def test_gemm_gated_against_float64(M, H, K, fmt, act, bias):
     (wg, g64), (wu, u64) = weight(g, H, K, bias), weight(g, H, K, bias)
     h = ops.gemm_gated(*a, wg, wu, act=act)
     assert ops.poll_status() == 0 and "+gated->bf16" in ops.last_path()
-    assert ops.last_path().startswith("rows") == on_few_rows(M, H, gated=True)
+    assert ops.last_path().startswith("rows") == on_few_rows(M, H, fmt, gated=True)
     check_gated(h, a64, g64, wg.bias, u64, wu.bias, act, "M=%d H=%d K=%d %s %s" % (M, H, K, fmt, act))
     if H % 32 == 0:
         for of in ("e2m1", "e4m3"):  # the bits of the activation quantizer, padding included
