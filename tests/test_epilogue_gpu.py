@@ -368,6 +368,35 @@ def test_gated_ffn_adds_onto_its_own_input(M):
     assert torch.equal(x, want) and ops.poll_status() == 0
 
 
+@pytest.mark.parametrize("M", [1, 48, 200])
+def test_operands_written_right_before_the_call(M):
+    """Kernels that start while the one before them ends see what the stream wrote before the call:
+    x, the weights and the residual change between calls that follow each other at once."""
+    ops = _ops()
+    g = gen(M + 11)
+    K, H = 1024, 768
+    sets = [[weight(g, H, K)[0], weight(g, H, K)[0], weight(g, K, H)[0], weight(g, K, K)[0], normal(g, M, K),
+             normal(g, M, K)] for _ in range(2)]
+    want = [(ops.linear_residual(s[4], s[3], "e4m3", residual=s[5]), ops.gated_ffn(s[4], *s[:3], residual=s[5]))
+            for s in sets]
+    cur = [ops.QWeight(w.codes.clone(), w.sf.clone(), w.N, w.K, w.bias.clone()) for w in sets[0][:4]]
+    x, r = sets[0][4].clone(), sets[0][5].clone()
+    got = []
+    for i in range(12):
+        s = sets[i % 2]
+        for c, w in zip(cur, s[:4]):
+            c.codes.copy_(w.codes)
+            c.sf.copy_(w.sf)
+            c.bias.copy_(w.bias)
+        x.copy_(s[4])
+        r.copy_(s[5])
+        y = ops.linear_residual(x, cur[3], "e4m3", residual=r)
+        got.append((y, ops.gated_ffn(x, *cur[:3], residual=r)))
+    assert ops.poll_status() == 0
+    for i, (y, f) in enumerate(got):
+        assert torch.equal(y, want[i % 2][0]) and torch.equal(f, want[i % 2][1]), i
+
+
 @pytest.mark.parametrize("M", [64, 300])
 def test_a_call_on_another_stream_keeps_its_workspace(M):
     """The workspace that a call allocates belongs to the stream it runs on: what the current stream
