@@ -9,8 +9,9 @@
 // with LayerNorm(v) = (v - mean) / sqrt(mean((v - mean)^2) + eps), RMSNorm(v) = v /
 // sqrt(mean(v^2) + eps), each times its weight plus its bias where given.  Everything between
 // the loads and the two roundings is binary32, the statistics taken in two passes over the
-// row in registers (first the mean, then the centered squares), so a large common offset
-// costs no digits.
+// row in registers (first the mean, then the centered squares) and the mean of an fp32 row far
+// from zero in a second round, so a large common offset costs no digits and a constant row
+// normalizes to zeros.
 //
 // A CTA holds its rows in registers: x and y are read once and z and h written once, which is
 // all the traffic there is; HBM bounds it.  The per-channel vectors (gate, scale, shift, weights)
@@ -214,13 +215,27 @@ __device__ __forceinline__ void block_sum(float (&v)[R], float* red)
     }
 }
 
+// A mean beyond this many standard deviations is taken again (row_stats).
+constexpr float kFarMean = 16.0f;
+
 // -mean (0 for RMSNorm) and 1 / sqrt(variance + eps) of the CTA's rows.  Channels past K (`live`
 // false; with kFull there are none) are held as zeros and left out of the centered squares.
 // load(r, j, t) gives chunk j of row r.
-template <int R, int C, bool kFull, class F>
-__device__ __forceinline__ void row_stats(F load, const bool (&live)[C][2], int kind, float inv_k, float eps,
-                                          float* red, float (&neg_mean)[R], float (&rstd)[R])
+// An error of the mean is multiplied by 1 / sqrt(variance + eps), a thousandfold in a constant row,
+// which has to come out as zeros.  kBf16 (the values are): values of like size, up to 2^15 of them of
+// eight bits, sum exactly, and one residual step after the product with the rounded 1 / K (Markstein's
+// division) gives the quotient, rounded once; a constant row's mean is exact.  Otherwise the sum is
+// rounded as well; so where the mean is far (rare; all threads agree, and row by row, so that a row's
+// result does not depend on its neighbours) the centered values, which are small, are summed too and
+// their mean is added: -mean is then neg_mean + lo[r] to about twice binary32's digits.  (For the fp32
+// stream this costs 1 to 3 %; for bf16 it would cost 10 % at 5120 channels, in spills.)
+template <bool kBf16, int R, int C, bool kFull, class F>
+__device__ __forceinline__ void row_stats(F load, const bool (&live)[C][2], int kind, uint32_t K, float inv_k,
+                                          float eps, float* red, float (&neg_mean)[R], float (&lo)[R],
+                                          float (&rstd)[R])
 {
+#pragma unroll
+    for (int r = 0; r < R; ++r) lo[r] = 0.0f;
     float2 t[4];
     if (kind == MXQ_NORM_LAYER) {
         float s[R];
@@ -237,7 +252,10 @@ __device__ __forceinline__ void row_stats(F load, const bool (&live)[C][2], int 
         }
         block_sum<R>(s, red);
 #pragma unroll
-        for (int r = 0; r < R; ++r) neg_mean[r] = -(s[r] * inv_k);
+        for (int r = 0; r < R; ++r) {
+            neg_mean[r] = -(s[r] * inv_k);
+            if constexpr (kBf16) neg_mean[r] = fmaf(-fmaf(neg_mean[r], static_cast<float>(K), s[r]), inv_k, neg_mean[r]);
+        }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             float2 q = make_float2(0.0f, 0.0f);
@@ -268,6 +286,57 @@ __device__ __forceinline__ void row_stats(F load, const bool (&live)[C][2], int 
         }
     }
     block_sum<R>(rstd, red + R * kMaxWarps);
+    if (!kBf16 && kind == MXQ_NORM_LAYER) {
+        bool far[R], any = false;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            far[r] = neg_mean[r] * neg_mean[r] > kFarMean * kFarMean * inv_k * rstd[r];
+            any = any || far[r];
+        }
+        if (any) {
+            const float k = static_cast<float>(K);
+            float s[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                float2 a = make_float2(0.0f, 0.0f);
+#pragma unroll
+                for (int j = 0; j < C; ++j) {
+                    load(r, j, t);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float m = kFull || live[j][i / 2] ? neg_mean[r] : 0.0f;
+                        a = __fadd2_rn(a, __fadd2_rn(t[i], make_float2(m, m)));
+                    }
+                }
+                s[r] = a.x + a.y;
+            }
+            block_sum<R>(s, red);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const float d = __fdiv_rn(s[r], k), m = neg_mean[r] - d;
+                if (far[r]) {
+                    lo[r] = (neg_mean[r] - m) - d;  // what the sum rounded off
+                    neg_mean[r] = m;
+                }
+                float2 q = make_float2(0.0f, 0.0f);
+#pragma unroll
+                for (int j = 0; j < C; ++j) {
+                    load(r, j, t);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float mi = kFull || live[j][i / 2] ? neg_mean[r] : 0.0f;
+                        const float2 c = __fadd2_rn(t[i], make_float2(mi, mi));
+                        q = __ffma2_rn(c, c, q);
+                    }
+                }
+                s[r] = q.x + q.y;
+            }
+            block_sum<R>(s, red + R * kMaxWarps);
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                if (far[r]) rstd[r] = fmaxf(fmaf(-k * lo[r], lo[r], s[r]), 0.0f);
+        }
+    }
 #pragma unroll
     for (int r = 0; r < R; ++r) rstd[r] = __frsqrt_rn(rstd[r] * inv_k + eps);
 }
@@ -315,18 +384,21 @@ __device__ __forceinline__ void apply_vec(float2 (&v)[R][C][4], const Raw8<kVF32
     }
 }
 
-// v = (v + neg_mean) * rstd.
+// v = (v + neg_mean + lo) * rstd.
 template <int R, int C>
-__device__ __forceinline__ void normalize(float2 (&v)[R][C][4], const float (&neg_mean)[R], const float (&rstd)[R])
+__device__ __forceinline__ void normalize(float2 (&v)[R][C][4], const float (&neg_mean)[R], const float (&lo)[R],
+                                          const float (&rstd)[R])
 {
 #pragma unroll
-    for (int r = 0; r < R; ++r)
+    for (int r = 0; r < R; ++r) {
+        const float at0 = lo[r] == 0.0f ? 0.0f : lo[r] * rstd[r];
 #pragma unroll
         for (int j = 0; j < C; ++j)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                v[r][j][i] = __fmul2_rn(__fadd2_rn(v[r][j][i], make_float2(neg_mean[r], neg_mean[r])),
-                                        make_float2(rstd[r], rstd[r]));
+                v[r][j][i] = __ffma2_rn(__fadd2_rn(v[r][j][i], make_float2(neg_mean[r], neg_mean[r])),
+                                        make_float2(rstd[r], rstd[r]), make_float2(at0, at0));
+    }
 }
 
 // Writes one chunk of h: in bf16, or as MX codes and scale bytes.  c: its first channel.
@@ -462,7 +534,7 @@ __global__ void __maxnreg__(norm_regs(kF32, C, R, kEarly)) norm_residual_kernel(
         }
     }
 
-    float neg_mean[R], rstd[R];
+    float neg_mean[R], lo[R], rstd[R];
     if (p.y) {
         if (p.post != MXQ_NORM_NONE) {
             if constexpr (!kFull) {
@@ -472,8 +544,8 @@ __global__ void __maxnreg__(norm_regs(kF32, C, R, kEarly)) norm_residual_kernel(
                     for (int j = 0; j < C; ++j)
                         zero_dead(y[r][j], live[j][0], live[j][1]);
             }
-            row_stats<R, C, kFull>([&](int r, int j, float2(&t)[4]) { keep_packed(y[r][j]); widen8(y[r][j], t); }, live,
-                                   p.post, p.inv_k, p.eps, red + 2 * R * kMaxWarps, neg_mean, rstd);
+            row_stats<true, R, C, kFull>([&](int r, int j, float2(&t)[4]) { keep_packed(y[r][j]); widen8(y[r][j], t); }, live,
+                                   p.post, p.K, p.inv_k, p.eps, red + 2 * R * kMaxWarps, neg_mean, lo, rstd);
         }
         // z = x + gate * u, chunk by chunk
 #pragma unroll
@@ -483,7 +555,7 @@ __global__ void __maxnreg__(norm_regs(kF32, C, R, kEarly)) norm_residual_kernel(
 #pragma unroll
             for (int r = 0; r < R; ++r) widen8(y[r][j], u[r][0]);
             if (p.post != MXQ_NORM_NONE) {
-                normalize(u, neg_mean, rstd);
+                normalize(u, neg_mean, lo, rstd);
                 if (p.post_weight) apply_vec<kVF32>(u, p.post_weight, 0, a1, Mul());
                 if (p.post_bias) apply_vec<kVF32>(u, p.post_bias, 0, a1, Add());
             }
@@ -519,8 +591,8 @@ __global__ void __maxnreg__(norm_regs(kF32, C, R, kEarly)) norm_residual_kernel(
             for (int j = 0; j < C; ++j)
                 zero_dead(z[r][j], live[j][0], live[j][1]);
     }
-    row_stats<R, C, kFull>([&](int r, int j, float2(&t)[4]) { keep_packed(z[r][j]); widen8(z[r][j], t); }, live, p.norm,
-                           p.inv_k, p.eps, red, neg_mean, rstd);
+    row_stats<!kF32, R, C, kFull>([&](int r, int j, float2(&t)[4]) { keep_packed(z[r][j]); widen8(z[r][j], t); }, live, p.norm,
+                           p.K, p.inv_k, p.eps, red, neg_mean, lo, rstd);
     float2 v[R][C][4];  // h
 #pragma unroll
     for (int r = 0; r < R; ++r)
@@ -529,7 +601,7 @@ __global__ void __maxnreg__(norm_regs(kF32, C, R, kEarly)) norm_residual_kernel(
             keep_packed(z[r][j]);
             widen8(z[r][j], v[r][j]);
         }
-    normalize(v, neg_mean, rstd);
+    normalize(v, neg_mean, lo, rstd);
     if constexpr (kEarly) {
         if (p.weight) apply_vec<kVF32>(v, w_r, Mul());
         if (p.bias) apply_vec<kVF32>(v, b_r, Add());
