@@ -33,6 +33,21 @@ def _p(t) -> ctypes.c_void_p:
     return ctypes.c_void_p(0 if t is None else t.data_ptr())
 
 
+def _empty(shape, dtype, device, stream=None, returned=True) -> torch.Tensor:
+    """A new tensor for a call that runs on `stream` (None: the current one).  It comes from that
+    stream's memory: a block of the current stream's could still be read by what is queued there
+    while the call writes it, or be handed out again there while the call still uses it.  For a
+    tensor that is returned the current stream is noted as a user too, since the caller's code
+    reads it there after waiting for the call."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if returned:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def _cuda_bf16(t: torch.Tensor, name: str) -> None:
     if not (t.is_cuda and t.dtype == torch.bfloat16 and t.is_contiguous()):
         raise ValueError("%s must be a contiguous bf16 CUDA tensor" % name)
@@ -485,14 +500,14 @@ def _mx_bytes(rows: int, K: int, f: int):
             max(1, (rows + 127) // 128 * 128 * ((K // 32 + 3) // 4) * 4))
 
 
-def _codes_out(codes, sf, rows, K, f, dev):
+def _codes_out(codes, sf, rows, K, f, dev, stream):
     """The buffers of a quantized [rows, K] output: the caller's, checked, or new ones."""
     nc, ns = _mx_bytes(rows, K, f)
     for t, n, name in ((codes, nc, "codes"), (sf, ns, "sf")):
         if t is not None and not (t.dtype == torch.uint8 and t.is_contiguous() and t.numel() >= n and t.device == dev):
             raise ValueError("%s must be a contiguous uint8 tensor of at least %d bytes on %s" % (name, n, dev))
-    codes = torch.empty(nc, dtype=torch.uint8, device=dev) if codes is None else codes
-    sf = torch.empty(ns, dtype=torch.uint8, device=dev) if sf is None else sf
+    codes = _empty(nc, torch.uint8, dev, stream) if codes is None else codes
+    sf = _empty(ns, torch.uint8, dev, stream) if sf is None else sf
     return codes, sf
 
 
@@ -525,16 +540,16 @@ def norm_residual(x: torch.Tensor, y: torch.Tensor | None = None, norm="layer", 
     zp = 0
     if y is not None:
         if z is None:
-            z = torch.empty_like(x)
+            z = _empty(shape, xdt, dev, stream)
             zp = z.data_ptr()
         else:
             zp = _tensor(z, "z", xdt, shape, dev)
     elif z is not None:
         raise ValueError("z goes with y")
     if f == _lib.OUT_BF16:
-        out = _bf16_out(h, rows, K, dev, "h")
+        out = _bf16_out(h, rows, K, dev, stream, "h")
     else:
-        out, sf = _codes_out(codes, sf, rows, K, f, dev)
+        out, sf = _codes_out(codes, sf, rows, K, f, dev, stream)
     d = _lib.NormDesc(x.data_ptr(), _opt(y, "y", torch.bfloat16, shape, dev), rows, K, _VEC_DTYPES[xdt],
                       _VEC_DTYPES[vdt], _pick(_NORMS, norm, "norm"), _pick(_NORMS, post_norm, "post_norm"),
                       _opt(weight, "weight", vdt, (K,), dev), _opt(bias, "bias", vdt, (K,), dev),
@@ -599,18 +614,15 @@ def _workspace(ws, need, dev, stream):
     """The caller's workspace, or a new one that belongs to the stream its kernels run on (one of
     another stream could be handed out again while they still use it)."""
     if ws is None:
-        if stream is None:
-            return torch.empty(max(1, need), dtype=torch.uint8, device=dev)
-        with torch.cuda.stream(stream):
-            return torch.empty(max(1, need), dtype=torch.uint8, device=dev)
+        return _empty(max(1, need), torch.uint8, dev, stream, returned=False)
     if ws.device != dev or not ws.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on %s" % dev)
     return ws
 
 
-def _bf16_out(out, M, N, dev, name="out"):
+def _bf16_out(out, M, N, dev, stream, name="out"):
     if out is None:
-        return torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+        return _empty((M, N), torch.bfloat16, dev, stream)
     _tensor(out, name, torch.bfloat16, (M, N), dev)
     return out
 
@@ -631,7 +643,7 @@ def gemm_residual(a_codes, a_sf, fmt, M: int, K: int, w: QWeight, act="none", re
     _check_k(w, K)
     d = _qweight(w, "w", dev)
     e = _epilogue(act, residual, gate, rows_per_group, M, w.N, dev)
-    out = _bf16_out(out, M, w.N, dev)
+    out = _bf16_out(out, M, w.N, dev, stream)
     check(_lib.lib().mxq_gemm_residual(a_codes.data_ptr(), a_sf.data_ptr(), f, M, K, d.codes, d.sf, w.N, d.bias, e,
                                        out.data_ptr(), _raw_stream(stream, dev)), "mxq_gemm_residual")
     return out
@@ -646,7 +658,7 @@ def gemm_bf16_residual(a: torch.Tensor, b: torch.Tensor, bias: torch.Tensor | No
     N = b.shape[0]
     bp = _tensor(b, "b", torch.bfloat16, (N, K), dev)
     e = _epilogue(act, residual, gate, rows_per_group, M, N, dev)
-    out = _bf16_out(out, M, N, dev)
+    out = _bf16_out(out, M, N, dev, stream)
     check(_lib.lib().mxq_gemm_bf16_residual(a.data_ptr(), M, K, bp, N, _opt(bias, "bias", torch.bfloat16, (N,), dev),
                                             e, out.data_ptr(), _raw_stream(stream, dev)), "mxq_gemm_bf16_residual")
     return out
@@ -669,18 +681,18 @@ def linear_residual(x: torch.Tensor, w: QWeight, fmt="e2m1", act="none", residua
         nc, ns = _mx_bytes(M, K, f)
         workspace = _workspace(workspace, (nc + 255) // 256 * 256 + (ns + 255) // 256 * 256, dev, stream)
         ws, wsb = workspace.data_ptr(), workspace.nbytes
-    out = _bf16_out(out, M, w.N, dev)
+    out = _bf16_out(out, M, w.N, dev, stream)
     check(_lib.lib().mxq_linear_residual(x.data_ptr(), M, K, d.codes, d.sf, w.N, d.bias, f, e, ws, wsb,
                                          out.data_ptr(), _raw_stream(stream, dev)), "mxq_linear_residual")
     return out
 
 
-def _gated_out(M, H, out_fmt, out, codes, sf, dev):
+def _gated_out(M, H, out_fmt, out, codes, sf, dev, stream):
     """(out_fmt, h or codes, scales or None) of a gated GEMM."""
     f = _pick(_OUTS, out_fmt, "out_fmt")
     if f == _lib.OUT_BF16:
-        return f, _bf16_out(out, M, H, dev), None
-    codes, sf = _codes_out(codes, sf, M, H, f, dev)
+        return f, _bf16_out(out, M, H, dev, stream), None
+    codes, sf = _codes_out(codes, sf, M, H, f, dev, stream)
     return f, codes, sf
 
 
@@ -692,7 +704,7 @@ def gemm_gated(a_codes, a_sf, fmt, M: int, K: int, gate: QWeight, up: QWeight, a
     f = _fmt(fmt)
     dev = _operand(a_codes, a_sf, M, K, f)
     dg, du = _qweight(gate, "gate", dev), _qweight(up, "up", dev)
-    of, o, so = _gated_out(M, gate.N, out_fmt, out, codes, sf, dev)
+    of, o, so = _gated_out(M, gate.N, out_fmt, out, codes, sf, dev, stream)
     check(_lib.lib().mxq_gemm_gated(a_codes.data_ptr(), a_sf.data_ptr(), f, M, K, dg, du, _act(act), of, o.data_ptr(),
                                     0 if so is None else so.data_ptr(), _raw_stream(stream, dev)), "mxq_gemm_gated")
     return o if so is None else (o, so)
@@ -706,7 +718,7 @@ def gemm_bf16_gated(a: torch.Tensor, gate: torch.Tensor, up: torch.Tensor, gate_
     H = gate.shape[0]
     gp, up_ = _tensor(gate, "gate", torch.bfloat16, (H, K), dev), _tensor(up, "up", torch.bfloat16, (H, K), dev)
     gb, ub = (_opt(b, n, torch.bfloat16, (H,), dev) for b, n in ((gate_bias, "gate_bias"), (up_bias, "up_bias")))
-    of, o, so = _gated_out(M, H, out_fmt, out, codes, sf, dev)
+    of, o, so = _gated_out(M, H, out_fmt, out, codes, sf, dev, stream)
     check(_lib.lib().mxq_gemm_bf16_gated(a.data_ptr(), M, K, gp, gb, up_, ub, H, _act(act), of, o.data_ptr(),
                                          0 if so is None else so.data_ptr(), _raw_stream(stream, dev)),
           "mxq_gemm_bf16_gated")
@@ -728,7 +740,7 @@ def gated_ffn(x: torch.Tensor, gate: QWeight, up: QWeight, down: QWeight, act="s
     uf, df = _fmt(up_fmt), _fmt(down_fmt)
     need = sum((n + 255) // 256 * 256 for n in _mx_bytes(M, K, uf) + _mx_bytes(M, gate.N, df))
     workspace = _workspace(workspace, need, dev, stream)
-    out = _bf16_out(out, M, down.N, dev)
+    out = _bf16_out(out, M, down.N, dev, stream)
     check(_lib.lib().mxq_gated_ffn(x.data_ptr(), M, K, dg, du, dd, _act(act), uf, df, e, workspace.data_ptr(),
                                    workspace.nbytes, out.data_ptr(),
                                    _raw_stream(stream, dev)), "mxq_gated_ffn")

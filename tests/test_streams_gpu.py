@@ -1,0 +1,100 @@
+"""Calls that are given a stream, run while the current stream is busy: outputs that they allocate
+are not memory that the current stream still reads or hands out again."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+M, K, H = 1000, 1024, 2048
+
+
+def _ops():
+    from fp8_mixed_precision_mxq_b200 import ops
+    return ops
+
+
+def around():
+    """The operators between a block's linears, each as a function of its stream."""
+    ops = _ops()
+    g = torch.Generator(device="cuda").manual_seed(1)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda").bfloat16()  # noqa: E731
+    x, y = rnd(M, K), rnd(M, K)
+    c, s = ops.quantize_act(x, "e4m3")
+    wg, wu, wd = ops.quantize_weight(rnd(H, K)), ops.quantize_weight(rnd(H, K)), ops.quantize_weight(rnd(K, H))
+    bg, bu = rnd(H, K), rnd(H, K)
+    return {
+        "norm": lambda st: ops.norm_residual(x, y, stream=st),
+        "norm e4m3": lambda st: ops.norm_residual(x, y, out_fmt="e4m3", stream=st),
+        "gemm": lambda st: ops.gemm_residual(c, s, "e4m3", M, K, wg, stream=st),
+        "gemm bf16": lambda st: ops.gemm_bf16_residual(x, bg, stream=st),
+        "linear": lambda st: ops.linear_residual(x, wg, stream=st),
+        "gated": lambda st: ops.gemm_gated(c, s, "e4m3", M, K, wg, wu, stream=st),
+        "gated e2m1": lambda st: ops.gemm_gated(c, s, "e4m3", M, K, wg, wu, out_fmt="e2m1", stream=st),
+        "gated bf16": lambda st: ops.gemm_bf16_gated(x, bg, bu, stream=st),
+        "ffn": lambda st: ops.gated_ffn(x, wg, wu, wd, stream=st),
+    }
+
+
+NAMES = ("norm", "norm e4m3", "gemm", "gemm bf16", "linear", "gated", "gated e2m1", "gated bf16", "ffn")
+
+
+def tensors(out):
+    return list(out) if isinstance(out, (tuple, list)) else [out]
+
+
+def check(call):
+    want = [t.clone() for t in tensors(call(None))]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        # blocks of the outputs' sizes, freed while the current stream has yet to read them
+        old = [torch.full((t.nbytes,), 0x3C, dtype=torch.uint8, device="cuda") for t in want]
+        room = [torch.empty_like(o) for o in old]
+        torch.cuda.synchronize()
+        torch.cuda._sleep(20_000_000)
+        for o, r in zip(old, room):
+            r.copy_(o)
+        del o, old
+        got = tensors(call(side))
+        # what the current stream allocates and writes behind the call is other memory too
+        junk = [torch.full((t.nbytes,), 0xFF, dtype=torch.uint8, device="cuda") for t in want]
+        torch.cuda.synchronize()
+        for r in room:
+            assert (r == 0x3C).all(), "the call wrote what the current stream still had to read"
+        for t, w in zip(got, want):
+            assert torch.equal(t, w)
+        del got, junk, room
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_outputs_on_another_stream(name):
+    check(around()[name])
+    assert _ops().poll_status() == 0
+
+
+def test_a_chain_on_another_stream_keeps_its_intermediates():
+    """Codes and scales that go out of scope while the stream still reads them."""
+    ops = _ops()
+    g = torch.Generator(device="cuda").manual_seed(2)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda").bfloat16()  # noqa: E731
+    x, y = rnd(M, K), rnd(M, K)
+    wg, wu, wd = ops.quantize_weight(rnd(H, K)), ops.quantize_weight(rnd(H, K)), ops.quantize_weight(rnd(K, H))
+
+    def chain(st):
+        z, c, s = ops.norm_residual(x, y, out_fmt="e4m3", stream=st)
+        c, s = ops.gemm_gated(c, s, "e4m3", M, K, wg, wu, out_fmt="e2m1", stream=st)
+        return ops.gemm_residual(c, s, "e2m1", M, H, wd, residual=z, stream=st)
+
+    want = chain(None)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    sizes = {n for f in ("e4m3", "e2m1") for w in (K, H) for n in ops._mx_bytes(M, w, ops._fmt(f))} | {M * K * 2}
+    for _ in range(5):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(5_000_000)
+        got = chain(side)
+        junk = [torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(2)]
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+        del got, junk
+    assert ops.poll_status() == 0
