@@ -1,7 +1,9 @@
 """Tensor-level entry points: the same calls as the C ABI (include/mxq.h), taking torch
-tensors for device memory and the current torch stream.  Nothing here computes:
-each function checks dtypes and devices, allocates outputs with torch, and calls the
-library."""
+tensors for device memory and the current torch stream, or the one given as `stream`.
+Nothing here computes: each function checks dtypes and devices, allocates outputs with
+torch (on the stream of the call), and calls the library.  As with any work on another
+stream, the caller orders a given stream behind whatever wrote the call's tensors, waits
+for it before using the result elsewhere, and keeps the tensors it passed until then."""
 from __future__ import annotations
 
 import ctypes
@@ -85,9 +87,9 @@ def quantize_act(x: torch.Tensor, fmt="e2m1", codes=None, sf=None, stream=None):
     M, K = x.shape
     f = _fmt(fmt)
     if codes is None:
-        codes = torch.empty(max(1, codes_bytes(M, K, f)), dtype=torch.uint8, device=x.device)
+        codes = _empty(max(1, codes_bytes(M, K, f)), torch.uint8, x.device, stream)
     if sf is None:
-        sf = torch.empty(max(1, sf_bytes(M, K)), dtype=torch.uint8, device=x.device)
+        sf = _empty(max(1, sf_bytes(M, K)), torch.uint8, x.device, stream)
     check(_lib.lib().mxq_quantize_act(_p(x), M, K, f, _p(codes), _p(sf), _stream(stream)), "mxq_quantize_act")
     return codes, sf
 
@@ -96,8 +98,8 @@ def quantize_weight(w: torch.Tensor, bias: torch.Tensor | None = None, stream=No
     """w [N, K] bf16 -> QWeight (MXFP4 codes [N, K/2] + tiled scales)."""
     _cuda_bf16(w, "w")
     N, K = w.shape
-    codes = torch.empty((N, K // 2), dtype=torch.uint8, device=w.device)
-    sf = torch.empty(max(1, sf_bytes(N, K)), dtype=torch.uint8, device=w.device)
+    codes = _empty((N, K // 2), torch.uint8, w.device, stream)
+    sf = _empty(max(1, sf_bytes(N, K)), torch.uint8, w.device, stream)
     check(_lib.lib().mxq_quantize_weight(_p(w), N, K, _p(codes), _p(sf), _stream(stream)), "mxq_quantize_weight")
     if bias is not None:
         _cuda_bf16(bias, "bias")
@@ -106,7 +108,7 @@ def quantize_weight(w: torch.Tensor, bias: torch.Tensor | None = None, stream=No
 
 def dequantize(codes: torch.Tensor, sf: torch.Tensor, rows: int, K: int, fmt="e2m1", out=None, stream=None):
     if out is None:
-        out = torch.empty((rows, K), dtype=torch.bfloat16, device=codes.device)
+        out = _empty((rows, K), torch.bfloat16, codes.device, stream)
     check(_lib.lib().mxq_dequantize(_p(codes), _p(sf), rows, K, _fmt(fmt), _p(out), _stream(stream)),
           "mxq_dequantize")
     return out
@@ -115,7 +117,7 @@ def dequantize(codes: torch.Tensor, sf: torch.Tensor, rows: int, K: int, fmt="e2
 def gemm(a_codes, a_sf, fmt, M: int, K: int, w: QWeight, out=None, stream=None):
     """GEMM on an already-quantized activation: y [M, N] bf16."""
     if out is None:
-        out = torch.empty((M, w.N), dtype=torch.bfloat16, device=a_codes.device)
+        out = _empty((M, w.N), torch.bfloat16, a_codes.device, stream)
     check(_lib.lib().mxq_gemm(_p(a_codes), _p(a_sf), _fmt(fmt), M, K, _p(w.codes), _p(w.sf), w.N, _p(w.bias),
                               _p(out), _stream(stream)), "mxq_gemm")
     return out
@@ -133,7 +135,7 @@ def gemm_bf16(a: torch.Tensor, b: torch.Tensor, bias: torch.Tensor | None = None
     if b.shape[1] != K:
         raise ValueError("a is [%d, %d] but b is [%d, %d]" % (M, K, N, b.shape[1]))
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=a.device)
+        out = _empty((M, N), torch.bfloat16, a.device, stream)
     check(_lib.lib().mxq_gemm_bf16(_p(a), M, K, _p(b), N, _p(bias), _p(out), _stream(stream)), "mxq_gemm_bf16")
     return out
 
@@ -153,11 +155,11 @@ def gemm_bf16_quant_a(a: torch.Tensor, b: torch.Tensor, fmt="e2m1", bias: torch.
         raise ValueError("a is [%d, %d] but b is [%d, %d]" % (M, K, N, b.shape[1]))
     f = _fmt(fmt)
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=a.device)
+        out = _empty((M, N), torch.bfloat16, a.device, stream)
     if codes is None:
-        codes = torch.empty(max(1, codes_bytes(M, K, f)), dtype=torch.uint8, device=a.device)
+        codes = _empty(max(1, codes_bytes(M, K, f)), torch.uint8, a.device, stream)
     if sf is None:
-        sf = torch.empty(max(1, sf_bytes(M, K)), dtype=torch.uint8, device=a.device)
+        sf = _empty(max(1, sf_bytes(M, K)), torch.uint8, a.device, stream)
     check(_lib.lib().mxq_gemm_bf16_quant_a(_p(a), M, K, _p(b), N, _p(bias), _p(out), f, _p(codes), _p(sf),
                                            _stream(stream)), "mxq_gemm_bf16_quant_a")
     return out, codes, sf
@@ -170,9 +172,9 @@ def linear(x: torch.Tensor, w: QWeight, fmt="e2m1", mode="native", workspace=Non
     f, m = _fmt(fmt), _mode(mode)
     need = workspace_bytes(M, w.N, K, f, m)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        workspace = _empty(need, torch.uint8, x.device, stream, returned=False)
     if out is None:
-        out = torch.empty((M, w.N), dtype=torch.bfloat16, device=x.device)
+        out = _empty((M, w.N), torch.bfloat16, x.device, stream)
     check(_lib.lib().mxq_linear(_p(x), M, K, _p(w.codes), _p(w.sf), w.N, _p(w.bias), f, m, _p(workspace),
                                 workspace.numel() * workspace.element_size(), _p(out), _stream(stream)),
           "mxq_linear")
@@ -188,7 +190,7 @@ def linear_noalloc(x: torch.Tensor, w: QWeight, fmt="e2m1", out=None, stream=Non
     _cuda_bf16(x, "x")
     M, K = x.shape
     if out is None:
-        out = torch.empty((M, w.N), dtype=torch.bfloat16, device=x.device)
+        out = _empty((M, w.N), torch.bfloat16, x.device, stream)
     check(_lib.lib().mxq_linear_noalloc(_p(x), M, K, _p(w.codes), _p(w.sf), w.N, _p(w.bias), _fmt(fmt), _p(out),
                                         _stream(stream)), "mxq_linear_noalloc")
     return out
@@ -201,9 +203,9 @@ def gemm_gelu_quant(a_codes, a_sf, fmt, M: int, K: int, w: QWeight, out_fmt="e2m
     tensor as h to also receive the GELU output."""
     f = _fmt(out_fmt)
     if codes is None:
-        codes = torch.empty(max(1, codes_bytes(M, w.N, f)), dtype=torch.uint8, device=a_codes.device)
+        codes = _empty(max(1, codes_bytes(M, w.N, f)), torch.uint8, a_codes.device, stream)
     if sf is None:
-        sf = torch.empty(max(1, sf_bytes(M, w.N)), dtype=torch.uint8, device=a_codes.device)
+        sf = _empty(max(1, sf_bytes(M, w.N)), torch.uint8, a_codes.device, stream)
     if h is not None:
         _cuda_bf16(h, "h")
     check(_lib.lib().mxq_gemm_gelu_quant(_p(a_codes), _p(a_sf), _fmt(fmt), M, K, _p(w.codes), _p(w.sf), w.N,
@@ -222,9 +224,9 @@ def gemm_quant(a_codes, a_sf, fmt, M: int, K: int, w: QWeight, act="none", out_f
         raise ValueError("act must be 'none' or 'gelu', got %r" % (act,))
     f = _fmt(out_fmt)
     if codes is None:
-        codes = torch.empty(max(1, codes_bytes(M, w.N, f)), dtype=torch.uint8, device=a_codes.device)
+        codes = _empty(max(1, codes_bytes(M, w.N, f)), torch.uint8, a_codes.device, stream)
     if sf is None:
-        sf = torch.empty(max(1, sf_bytes(M, w.N)), dtype=torch.uint8, device=a_codes.device)
+        sf = _empty(max(1, sf_bytes(M, w.N)), torch.uint8, a_codes.device, stream)
     if h is not None:
         _cuda_bf16(h, "h")
     check(_lib.lib().mxq_gemm_quant(_p(a_codes), _p(a_sf), _fmt(fmt), M, K, _p(w.codes), _p(w.sf), w.N, _p(w.bias),
@@ -236,7 +238,7 @@ def gelu_bf16(x: torch.Tensor, out=None, stream=None) -> torch.Tensor:
     """GELU of bf16 values as the quantizing epilogue applies it (exact, rounded once to bf16)."""
     _cuda_bf16(x, "x")
     if out is None:
-        out = torch.empty_like(x)
+        out = _empty(x.shape, x.dtype, x.device, stream)
     _cuda_bf16(out, "out")
     if out.numel() != x.numel():
         raise ValueError("out must have as many elements as x")
@@ -255,10 +257,10 @@ def ffn(x: torch.Tensor, up: QWeight, down: QWeight, up_fmt="e2m1", down_fmt="e2
     _cuda_bf16(x, "x")
     M, K = x.shape
     if workspace is None:
-        workspace = torch.empty(ffn_workspace_bytes(M, K, up.N, up_fmt, down_fmt), dtype=torch.uint8,
-                                device=x.device)
+        workspace = _empty(ffn_workspace_bytes(M, K, up.N, up_fmt, down_fmt), torch.uint8, x.device, stream,
+                           returned=False)
     if out is None:
-        out = torch.empty((M, down.N), dtype=torch.bfloat16, device=x.device)
+        out = _empty((M, down.N), torch.bfloat16, x.device, stream)
     du, dd = up.desc(), down.desc()
     check(_lib.lib().mxq_ffn(_p(x), M, K, ctypes.byref(du), ctypes.byref(dd), _fmt(up_fmt), _fmt(down_fmt),
                              _p(workspace), workspace.numel(), _p(out), _stream(stream)), "mxq_ffn")
@@ -269,7 +271,7 @@ def absmax(x: torch.Tensor, out=None, stream=None) -> torch.Tensor:
     """max |x| over a bf16 tensor, as a one-element fp32 CUDA tensor (calibration)."""
     _cuda_bf16(x, "x")
     if out is None:
-        out = torch.empty(1, dtype=torch.float32, device=x.device)
+        out = _empty(1, torch.float32, x.device, stream)
     check(_lib.lib().mxq_absmax(_p(x), x.numel(), _p(out), _stream(stream)), "mxq_absmax")
     return out
 
@@ -279,9 +281,9 @@ def quantize_act_static(x: torch.Tensor, scale: float, codes=None, sf=None, stre
     _cuda_bf16(x, "x")
     M, K = x.shape
     if codes is None:
-        codes = torch.empty(max(1, codes_bytes(M, K, FMT_E4M3)), dtype=torch.uint8, device=x.device)
+        codes = _empty(max(1, codes_bytes(M, K, FMT_E4M3)), torch.uint8, x.device, stream)
     if sf is None:
-        sf = torch.empty(max(1, sf_bytes(M, K)), dtype=torch.uint8, device=x.device)
+        sf = _empty(max(1, sf_bytes(M, K)), torch.uint8, x.device, stream)
     check(_lib.lib().mxq_quantize_act_static(_p(x), M, K, float(scale), _p(codes), _p(sf), _stream(stream)),
           "mxq_quantize_act_static")
     return codes, sf
@@ -292,10 +294,10 @@ def linear_static(x: torch.Tensor, w: QWeight, act_scale: float, workspace=None,
     _cuda_bf16(x, "x")
     M, K = x.shape
     if workspace is None:
-        workspace = torch.empty(workspace_bytes(M, w.N, K, FMT_E4M3, MODE_NATIVE), dtype=torch.uint8,
-                                device=x.device)
+        workspace = _empty(workspace_bytes(M, w.N, K, FMT_E4M3, MODE_NATIVE), torch.uint8, x.device, stream,
+                           returned=False)
     if out is None:
-        out = torch.empty((M, w.N), dtype=torch.bfloat16, device=x.device)
+        out = _empty((M, w.N), torch.bfloat16, x.device, stream)
     check(_lib.lib().mxq_linear_static(_p(x), M, K, _p(w.codes), _p(w.sf), w.N, _p(w.bias), float(act_scale),
                                        _p(workspace), workspace.numel(), _p(out), _stream(stream)),
           "mxq_linear_static")
@@ -317,9 +319,9 @@ def quantize_act_transformed(x: torch.Tensor, fmt="e2m1", block=32, mul=None, co
     f = _fmt(fmt)
     mul = _f32_or_none(mul, "mul")
     if codes is None:
-        codes = torch.empty(max(1, codes_bytes(M, K, f)), dtype=torch.uint8, device=x.device)
+        codes = _empty(max(1, codes_bytes(M, K, f)), torch.uint8, x.device, stream)
     if sf is None:
-        sf = torch.empty(max(1, sf_bytes(M, K)), dtype=torch.uint8, device=x.device)
+        sf = _empty(max(1, sf_bytes(M, K)), torch.uint8, x.device, stream)
     check(_lib.lib().mxq_quantize_act_transformed(_p(x), M, K, f, _p(mul), int(block), _p(codes), _p(sf),
                                                   _stream(stream)), "mxq_quantize_act_transformed")
     return codes, sf
@@ -330,8 +332,8 @@ def quantize_weight_transformed(w: torch.Tensor, bias=None, block=32, mul=None, 
     _cuda_bf16(w, "w")
     N, K = w.shape
     mul = _f32_or_none(mul, "mul")
-    codes = torch.empty((N, K // 2), dtype=torch.uint8, device=w.device)
-    sf = torch.empty(max(1, sf_bytes(N, K)), dtype=torch.uint8, device=w.device)
+    codes = _empty((N, K // 2), torch.uint8, w.device, stream)
+    sf = _empty(max(1, sf_bytes(N, K)), torch.uint8, w.device, stream)
     check(_lib.lib().mxq_quantize_weight_transformed(_p(w), N, K, _p(mul), int(block), _p(codes), _p(sf),
                                                      _stream(stream)), "mxq_quantize_weight_transformed")
     if bias is not None:
@@ -347,9 +349,10 @@ def linear_transformed(x: torch.Tensor, w: QWeight, fmt="e2m1", block=32, act_mu
     f = _fmt(fmt)
     act_mul = _f32_or_none(act_mul, "act_mul")
     if workspace is None:
-        workspace = torch.empty(workspace_bytes(M, w.N, K, f, MODE_NATIVE), dtype=torch.uint8, device=x.device)
+        workspace = _empty(workspace_bytes(M, w.N, K, f, MODE_NATIVE), torch.uint8, x.device, stream,
+                           returned=False)
     if out is None:
-        out = torch.empty((M, w.N), dtype=torch.bfloat16, device=x.device)
+        out = _empty((M, w.N), torch.bfloat16, x.device, stream)
     check(_lib.lib().mxq_linear_transformed(_p(x), M, K, _p(w.codes), _p(w.sf), w.N, _p(w.bias), f, _p(act_mul),
                                             int(block), _p(workspace), workspace.numel(), _p(out), _stream(stream)),
           "mxq_linear_transformed")
@@ -369,9 +372,9 @@ def lowrank_split(w: torch.Tensor, U: torch.Tensor, S: torch.Tensor, Vh: torch.T
     if U.shape[0] != N or Vh.shape[1] != K or min(U.shape[1], S.shape[0], Vh.shape[0]) < rank:
         raise ValueError("factors of shapes %s, %s, %s do not fit w [%d, %d] at rank %d" % (
             tuple(U.shape), tuple(S.shape), tuple(Vh.shape), N, K, rank))
-    l2t = torch.empty((N, rank), dtype=torch.bfloat16, device=w.device)
-    l1t = torch.empty((rank, K), dtype=torch.bfloat16, device=w.device)
-    resid = torch.empty((N, K), dtype=torch.bfloat16, device=w.device)
+    l2t = _empty((N, rank), torch.bfloat16, w.device, stream)
+    l1t = _empty((rank, K), torch.bfloat16, w.device, stream)
+    resid = _empty((N, K), torch.bfloat16, w.device, stream)
     check(_lib.lib().mxq_lowrank_split(_p(U), U.stride(0), _p(S), _p(Vh), Vh.stride(0), _p(w), N, K, rank, _p(l2t),
                                        _p(l1t), _p(resid), _stream(stream)), "mxq_lowrank_split")
     return l1t, l2t, resid
@@ -383,8 +386,15 @@ def svd_split(w: torch.Tensor, rank: int, stream=None):
     the split into l2t = U_r sqrt(S_r), l1t = sqrt(S_r) V_r^T and the bf16 residual
     w - l2t . l1t runs in this library (lowrank_split).  Returns (l1t, l2t, residual)."""
     _cuda_bf16(w, "w")
+    if stream is not None:  # the decomposition runs there too
+        caller = torch.cuda.current_stream(w.device)
+        with torch.cuda.stream(stream):
+            parts = svd_split(w, rank)
+        for t in parts:
+            t.record_stream(caller)
+        return parts
     U, S, Vh = torch.linalg.svd(w.float(), full_matrices=False)
-    return lowrank_split(w, U.contiguous(), S.contiguous(), Vh.contiguous(), rank, stream=stream)
+    return lowrank_split(w, U.contiguous(), S.contiguous(), Vh.contiguous(), rank)
 
 
 def channel_absmax(x: torch.Tensor, out=None, stream=None) -> torch.Tensor:
@@ -392,7 +402,7 @@ def channel_absmax(x: torch.Tensor, out=None, stream=None) -> torch.Tensor:
     _cuda_bf16(x, "x")
     rows, K = x.shape
     if out is None:
-        out = torch.empty(K, dtype=torch.float32, device=x.device)
+        out = _empty(K, torch.float32, x.device, stream)
     check(_lib.lib().mxq_channel_absmax(_p(x), rows, K, _p(out), _stream(stream)), "mxq_channel_absmax")
     return out
 
@@ -406,8 +416,8 @@ def smooth_scales(amax_x: torch.Tensor, amax_w: torch.Tensor, alpha: float = 0.5
     K = amax_x.numel()
     if amax_w.numel() != K:
         raise ValueError("channel counts differ: %d vs %d" % (K, amax_w.numel()))
-    s = torch.empty(K, dtype=torch.float32, device=amax_x.device)
-    inv = torch.empty(K, dtype=torch.float32, device=amax_x.device) if with_inverse else None
+    s = _empty(K, torch.float32, amax_x.device, stream)
+    inv = _empty(K, torch.float32, amax_x.device, stream) if with_inverse else None
     check(_lib.lib().mxq_smooth_scales(_p(amax_x), _p(amax_w), K, float(alpha), _p(s), _p(inv), _stream(stream)),
           "mxq_smooth_scales")
     return (s, inv) if with_inverse else s
@@ -425,7 +435,7 @@ def sqnr(refs, tests, out=None, stream=None) -> torch.Tensor:
         if r.numel() != t.numel():
             raise ValueError("a reference and its test tensor differ in size")
     if out is None:
-        out = torch.empty(3, dtype=torch.float64, device=refs[0].device)
+        out = _empty(3, torch.float64, refs[0].device, stream)
     n = len(refs)
     rp = (ctypes.c_void_p * n)(*[r.data_ptr() for r in refs])
     tp = (ctypes.c_void_p * n)(*[t.data_ptr() for t in tests])
@@ -762,10 +772,10 @@ def linear_lowrank(x: torch.Tensor, residual: QWeight, l1t: torch.Tensor, l2t: t
     rank = l1t.shape[0]
     f = _fmt(fmt)
     if workspace is None:
-        workspace = torch.empty(lowrank_workspace_bytes(M, residual.N, K, f, rank), dtype=torch.uint8,
-                                device=x.device)
+        workspace = _empty(lowrank_workspace_bytes(M, residual.N, K, f, rank), torch.uint8, x.device, stream,
+                           returned=False)
     if out is None:
-        out = torch.empty((M, residual.N), dtype=torch.bfloat16, device=x.device)
+        out = _empty((M, residual.N), torch.bfloat16, x.device, stream)
     check(_lib.lib().mxq_linear_lowrank(_p(x), M, K, _p(residual.codes), _p(residual.sf), residual.N,
                                         _p(residual.bias), f, _p(l1t), _p(l2t), rank, _p(workspace),
                                         workspace.numel(), _p(out), _stream(stream)), "mxq_linear_lowrank")
@@ -789,10 +799,10 @@ def dit_block_linears(weights, xs, w4a8_bits: int, mode="native", workspace=None
     for x in xs:
         _cuda_bf16(x, "block input")
     if outs is None:
-        outs = [torch.empty((r, w.N), dtype=torch.bfloat16, device=xs[0].device) for r, w in zip(rows, weights)]
+        outs = [_empty((r, w.N), torch.bfloat16, xs[0].device, stream) for r, w in zip(rows, weights)]
     need = block_workspace_bytes(weights, rows, w4a8_bits, mode)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=xs[0].device)
+        workspace = _empty(need, torch.uint8, xs[0].device, stream, returned=False)
     descs = (WDesc * 8)(*[w.desc() for w in weights])
     xin = (ctypes.c_void_p * 8)(*[x.data_ptr() for x in xs])
     ms = (ctypes.c_int64 * 8)(*rows)
@@ -803,7 +813,7 @@ def dit_block_linears(weights, xs, w4a8_bits: int, mode="native", workspace=None
 
 
 def sf_to_logical(sf: torch.Tensor, rows: int, K: int, stream=None) -> torch.Tensor:
-    out = torch.empty((rows, K // 32), dtype=torch.uint8, device=sf.device)
+    out = _empty((rows, K // 32), torch.uint8, sf.device, stream)
     check(_lib.lib().mxq_sf_to_logical(_p(sf), rows, K, _p(out), _stream(stream)), "mxq_sf_to_logical")
     return out
 

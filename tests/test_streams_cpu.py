@@ -88,6 +88,43 @@ AROUND = {  # what a transformer block computes between its linears
 }
 
 
+W, W8 = weight(H, K), [weight(K, K)] * 6 + [weight(H, K), weight(K, H)]
+ROWS8 = [X] * 7 + [torch.zeros(M, H, dtype=BF16)]
+L1, L2 = torch.zeros(64, K, dtype=BF16), torch.zeros(H, 64, dtype=BF16)
+V = torch.zeros(K, dtype=F32)
+EARLIER = {  # quantizers, linears and calibration
+    "quantize_act": lambda s: ops.quantize_act(X, stream=s),
+    "quantize_weight": lambda s: parts(ops.quantize_weight(X, stream=s)),
+    "dequantize": lambda s: ops.dequantize(XC, XS, M, K, "e4m3", stream=s),
+    "gemm": lambda s: ops.gemm(XC, XS, "e4m3", M, K, W, stream=s),
+    "gemm_bf16": lambda s: ops.gemm_bf16(X, torch.zeros(H, K, dtype=BF16), stream=s),
+    "gemm_bf16_quant_a": lambda s: ops.gemm_bf16_quant_a(X, L1, stream=s),
+    "linear": lambda s: ops.linear(X, W, stream=s),
+    "linear qdq": lambda s: ops.linear(X, W, mode="qdq", stream=s),
+    "linear_noalloc": lambda s: ops.linear_noalloc(X, W, stream=s),
+    "gemm_gelu_quant": lambda s: ops.gemm_gelu_quant(XC, XS, "e4m3", M, K, W, stream=s),
+    "gemm_quant": lambda s: ops.gemm_quant(XC, XS, "e4m3", M, K, W, stream=s),
+    "gelu_bf16": lambda s: ops.gelu_bf16(X, stream=s),
+    "ffn": lambda s: ops.ffn(X, W, weight(K, H), stream=s),
+    "absmax": lambda s: ops.absmax(X, stream=s),
+    "quantize_act_static": lambda s: ops.quantize_act_static(X, 1.0, stream=s),
+    "linear_static": lambda s: ops.linear_static(X, W, 1.0, stream=s),
+    "quantize_act_transformed": lambda s: ops.quantize_act_transformed(X, stream=s),
+    "quantize_weight_transformed": lambda s: parts(ops.quantize_weight_transformed(X, stream=s)),
+    "linear_transformed": lambda s: ops.linear_transformed(X, W, stream=s),
+    "channel_absmax": lambda s: ops.channel_absmax(X, stream=s),
+    "smooth_scales": lambda s: ops.smooth_scales(V, V, with_inverse=True, stream=s),
+    "sqnr": lambda s: ops.sqnr([X], [X], stream=s),
+    "linear_lowrank": lambda s: ops.linear_lowrank(X, W, L1, L2, stream=s),
+    "dit_block_linears": lambda s: ops.dit_block_linears(W8, ROWS8, 0x0F, stream=s),
+    "sf_to_logical": lambda s: ops.sf_to_logical(XS, M, K, stream=s),
+}
+
+
+def parts(w):
+    return w.codes, w.sf
+
+
 def check(call, streams):
     side, current, lib, log = streams
     out = call(side)
@@ -104,3 +141,19 @@ def check(call, streams):
 @pytest.mark.parametrize("name", AROUND)
 def test_a_call_on_a_stream_allocates_there(name, streams):
     check(AROUND[name], streams)
+
+
+@pytest.mark.parametrize("name", EARLIER)
+def test_a_quantizer_or_linear_on_a_stream_allocates_there(name, streams):
+    check(EARLIER[name], streams)
+
+
+def test_a_split_on_a_stream_is_decomposed_there(streams, monkeypatch):
+    side, current, lib, log = streams
+    where = []
+    svd = lambda w, full_matrices: where.append(list(log["under"])) or (w, w[0], w)  # noqa: E731
+    monkeypatch.setattr(torch.linalg, "svd", svd)
+    monkeypatch.setattr(ops, "lowrank_split", lambda w, U, S, Vh, rank: where.append(list(log["under"])) or (U, Vh, w))
+    out = ops.svd_split(X, 4, stream=side)
+    assert where == [[side], [side]]
+    assert all(any(t is n and s is current for n, s in log["noted"]) for t in out)

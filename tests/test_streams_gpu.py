@@ -98,3 +98,42 @@ def test_a_chain_on_another_stream_keeps_its_intermediates():
         assert torch.equal(got, want)
         del got, junk
     assert ops.poll_status() == 0
+
+
+def earlier():
+    """Quantizers and linears, each as a function of its stream."""
+    ops = _ops()
+    g = torch.Generator(device="cuda").manual_seed(3)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda").bfloat16()  # noqa: E731
+    x = rnd(M, K)
+    c, s = ops.quantize_act(x, "e4m3")
+    w, wd = ops.quantize_weight(rnd(H, K)), ops.quantize_weight(rnd(K, H))
+    l1, l2 = rnd(64, K), rnd(H, 64)
+    return {
+        "quantize": lambda st: ops.quantize_act(x, stream=st),
+        "dequantize": lambda st: ops.dequantize(c, s, M, K, "e4m3", stream=st),
+        "gemm": lambda st: ops.gemm(c, s, "e4m3", M, K, w, stream=st),
+        "linear": lambda st: ops.linear(x, w, stream=st),
+        "linear qdq": lambda st: ops.linear(x, w, mode="qdq", stream=st),
+        "ffn": lambda st: ops.ffn(x, w, wd, stream=st),
+        "lowrank": lambda st: ops.linear_lowrank(x, w, l1, l2, stream=st),
+        "transformed": lambda st: ops.linear_transformed(x, w, stream=st),
+    }
+
+
+@pytest.mark.parametrize("name", ("quantize", "dequantize", "gemm", "linear", "linear qdq", "ffn", "lowrank",
+                                  "transformed"))
+def test_quantizers_and_linears_on_another_stream(name):
+    check(earlier()[name])
+    assert _ops().poll_status() == 0
+
+
+def test_split_on_another_stream():
+    ops = _ops()
+    w = torch.randn(96, 128, device="cuda").bfloat16()
+    want = ops.svd_split(w, 8)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = ops.svd_split(w, 8, stream=side)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
