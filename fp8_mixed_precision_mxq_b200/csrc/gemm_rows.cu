@@ -19,7 +19,8 @@
 // timing), and apply bias, activation, gate and residual, or the gated product and the MX
 // quantization (32 lanes = 32 consecutive outputs = one MX block).
 // Launches are programmatic: the set-up runs while the kernel before on the stream ends.  All
-// global reads and writes come after griddepcontrol.wait, except that behind a kernel of the same
+// global reads and writes come after griddepcontrol.wait (by plain loads: the non-coherent path is for
+// data that nothing writes while the kernel runs, and the compiler may move such a load), except that behind a kernel of the same
 // call (the quantizer of x, or the gated network's first kernel) the weight is read before it: the
 // quantizer is an ordinary launch and the first kernel lets this one start only after its own wait,
 // so whatever wrote the weight has completed.  (48 rows of 5120 x 13824 W4A8, quantizer included:
@@ -147,7 +148,7 @@ struct QuantX {
         for (int i = 0; i < kRounds; ++i) {
             const int unit = i * 128 + tid, row = unit / kLanes, k = ks * kKps + unit % kLanes * 8;
             raw[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (row < p.M && k < p.K) raw[i] = __ldg(reinterpret_cast<const uint4*>(p.x + static_cast<size_t>(row) * p.K + k));
+            if (row < p.M && k < p.K) raw[i] = *reinterpret_cast<const uint4*>(p.x + static_cast<size_t>(row) * p.K + k);
         }
     }
 
@@ -307,8 +308,8 @@ __global__ void __launch_bounds__(kThreads, 2)
             if (kGated || !live || t >= M) continue;
             if (p.gate != nullptr) {
                 const size_t gi = static_cast<size_t>(static_cast<uint32_t>(m0 + t) / p.rows_per_group) * p.N + n;
-                gate_r[i] = p.gate_f32 ? __ldg(static_cast<const uint32_t*>(p.gate) + gi)
-                                       : __ldg(static_cast<const uint16_t*>(p.gate) + gi);
+                gate_r[i] = p.gate_f32 ? static_cast<const uint32_t*>(p.gate)[gi]
+                                       : static_cast<const uint16_t*>(p.gate)[gi];
             }
             if (p.res != nullptr)
                 res_r[i] = reinterpret_cast<const uint16_t*>(p.res)[static_cast<size_t>(m0 + t) * p.N + n];
@@ -318,8 +319,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     auto load_epilogue = [&]() {
         load_four(first4);
         if (!live || 4 * first4 >= M) return;
-        if (p.bias != nullptr) bias_r[0] = __ldg(reinterpret_cast<const uint16_t*>(p.bias) + n);
-        if (kGated && p.bias2 != nullptr) bias_r[1] = __ldg(reinterpret_cast<const uint16_t*>(p.bias2) + n);
+        if (p.bias != nullptr) bias_r[0] = reinterpret_cast<const uint16_t*>(p.bias)[n];
+        if (kGated && p.bias2 != nullptr) bias_r[1] = reinterpret_cast<const uint16_t*>(p.bias2)[n];
     };
 
     if (warp == 0) {
