@@ -255,11 +255,25 @@ int check_act(int act)
     return MXQ_OK;
 }
 
-int check_epilogue(const mxq_epilogue* e)
+// An output of n bytes that shares memory with an input of m bytes: some CTAs would still read the
+// input while others write over it.
+int check_apart(const void* out, uint64_t n, const char* out_name, const void* in, uint64_t m, const char* in_name)
+{
+    const uintptr_t o = reinterpret_cast<uintptr_t>(out), i = reinterpret_cast<uintptr_t>(in);
+    if (o < i + m && i < o + n) return fail(MXQ_ERR_INVALID_ARG, "%s overlaps %s", out_name, in_name);
+    return MXQ_OK;
+}
+
+// e, and the [M, N] bf16 output y it goes into (which its residual may be, element for element).
+int check_epilogue(const mxq_epilogue* e, int64_t M, int64_t N, const void* y)
 {
     if (!e) return fail(MXQ_ERR_INVALID_ARG, "epilogue is NULL");
     RETURN_IF(check_act(e->act));
-    if (e->residual) RETURN_IF(check_ptr(e->residual, "residual"));
+    if (e->residual) {
+        RETURN_IF(check_ptr(e->residual, "residual"));
+        const uint64_t n = static_cast<uint64_t>(M) * N * 2;
+        if (e->residual != y) RETURN_IF(check_apart(y, n, "y", e->residual, n, "a residual that it is not"));
+    }
     if (e->gate) {
         RETURN_IF(check_dtype(e->gate_dtype, "gate_dtype"));
         RETURN_IF(check_ptr(e->gate, "gate"));
@@ -300,6 +314,19 @@ int run_gemm_residual(const void* a_codes, const void* a_sf, int a_fmt, int64_t 
 }
 
 // The output of a gated GEMM: h [M, H] in bf16, or its MX form (H is the next layer's K).
+// What a GEMM reads of a [M, K] operand while it writes `out`.
+int check_apart_mx(const void* out, uint64_t n, const char* out_name, const void* a_codes, const void* a_sf, int a_fmt,
+                   int64_t M, int64_t K)
+{
+    RETURN_IF(check_apart(out, n, out_name, a_codes, codes_bytes(M, K, a_fmt), "a_codes"));
+    return check_apart(out, n, out_name, a_sf, sf_bytes(M, K), "a_sf");
+}
+
+uint64_t gated_out_bytes(int64_t M, int64_t H, int out_fmt)
+{
+    return out_fmt == MXQ_OUT_BF16 ? static_cast<uint64_t>(M) * H * 2 : codes_bytes(M, H, out_fmt);
+}
+
 int check_gated_out(int64_t M, int64_t H, int act, int out_fmt, const void* out, const void* out_sf)
 {
     RETURN_IF(check_act(act));
@@ -1004,7 +1031,8 @@ int mxq_gemm_residual(const void* a_codes, const void* a_sf, int a_fmt, int64_t 
                       void* stream)
 {
     RETURN_IF(check_gemm(a_codes, a_sf, a_fmt, M, K, w_codes, w_sf, N, bias_bf16, y_bf16));
-    RETURN_IF(check_epilogue(e));
+    RETURN_IF(check_epilogue(e, M, N, y_bf16));
+    RETURN_IF(check_apart_mx(y_bf16, static_cast<uint64_t>(M) * N * 2, "y", a_codes, a_sf, a_fmt, M, K));
     RETURN_IF(check_device());
     return run_gemm_residual(a_codes, a_sf, a_fmt, M, K, w_codes, w_sf, N, bias_bf16, *e, y_bf16,
                              static_cast<cudaStream_t>(stream));
@@ -1014,7 +1042,8 @@ int mxq_gemm_bf16_residual(const void* a_bf16, int64_t M, int64_t K, const void*
                            const void* bias_bf16, const mxq_epilogue* e, void* y_bf16, void* stream)
 {
     RETURN_IF(check_gemm_bf16(a_bf16, M, K, b_bf16, N, bias_bf16, y_bf16));
-    RETURN_IF(check_epilogue(e));
+    RETURN_IF(check_epilogue(e, M, N, y_bf16));
+    RETURN_IF(check_apart(y_bf16, static_cast<uint64_t>(M) * N * 2, "y", a_bf16, static_cast<uint64_t>(M) * K * 2, "a"));
     RETURN_IF(check_device());
     GemmArgs g{a_bf16, nullptr, MXQ_FMT_E2M1, M, N, K, b_bf16, nullptr, bias_bf16, y_bf16};
     g.bf16 = true;
@@ -1031,16 +1060,14 @@ int mxq_linear_residual(const void* x_bf16, int64_t M, int64_t K, const void* w_
     if (!fused) RETURN_IF(check_ptr(workspace, "workspace", kWsAlign));
     // x stands in for the quantized activation in the GEMM checks
     RETURN_IF(check_gemm(x_bf16, x_bf16, act_fmt, M, K, w_codes, w_sf, N, bias_bf16, y_bf16));
-    RETURN_IF(check_epilogue(e));
+    RETURN_IF(check_epilogue(e, M, N, y_bf16));
     if (!fused) {
         const int64_t need = linear_ws(M, N, K, act_fmt, MXQ_MODE_NATIVE);
         if (ws_bytes < need)
             return fail(MXQ_ERR_WORKSPACE, "workspace has %lld bytes, needs %lld", (long long)ws_bytes, (long long)need);
     }
     // the fused kernel's CTAs read x while others write y
-    const uintptr_t xa = reinterpret_cast<uintptr_t>(x_bf16), ya = reinterpret_cast<uintptr_t>(y_bf16);
-    if (xa < ya + static_cast<uint64_t>(M) * N * 2 && ya < xa + static_cast<uint64_t>(M) * K * 2)
-        return fail(MXQ_ERR_INVALID_ARG, "linear with residual: y overlaps x");
+    RETURN_IF(check_apart(y_bf16, static_cast<uint64_t>(M) * N * 2, "y", x_bf16, static_cast<uint64_t>(M) * K * 2, "x"));
     RETURN_IF(check_device());
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (fused)
@@ -1061,6 +1088,8 @@ int mxq_gemm_gated(const void* a_codes, const void* a_sf, int a_fmt, int64_t M, 
     RETURN_IF(check_gated_out(M, gate->N, act, out_fmt, out, out_sf));
     RETURN_IF(check_gemm(a_codes, a_sf, a_fmt, M, K, gate->codes, gate->sf, gate->N, gate->bias, out));
     RETURN_IF(check_gemm(a_codes, a_sf, a_fmt, M, K, up->codes, up->sf, up->N, up->bias, out));
+    RETURN_IF(check_apart_mx(out, gated_out_bytes(M, gate->N, out_fmt), "out", a_codes, a_sf, a_fmt, M, K));
+    if (out_sf) RETURN_IF(check_apart_mx(out_sf, sf_bytes(M, gate->N), "out_sf", a_codes, a_sf, a_fmt, M, K));
     RETURN_IF(check_device());
     return run_gemm_gated(a_codes, a_sf, a_fmt, M, K, *gate, *up, act, out_fmt, out, out_sf,
                           static_cast<cudaStream_t>(stream));
@@ -1073,6 +1102,9 @@ int mxq_gemm_bf16_gated(const void* a_bf16, int64_t M, int64_t K, const void* ga
     RETURN_IF(check_gated_out(M, H, act, out_fmt, out, out_sf));
     RETURN_IF(check_gemm_bf16(a_bf16, M, K, gate_bf16, H, gate_bias, out));
     RETURN_IF(check_gemm_bf16(a_bf16, M, K, up_bf16, H, up_bias, out));
+    const uint64_t a_bytes = static_cast<uint64_t>(M) * K * 2;
+    RETURN_IF(check_apart(out, gated_out_bytes(M, H, out_fmt), "out", a_bf16, a_bytes, "a"));
+    if (out_sf) RETURN_IF(check_apart(out_sf, sf_bytes(M, H), "out_sf", a_bf16, a_bytes, "a"));
     RETURN_IF(check_device());
     GemmArgs g{a_bf16, nullptr, MXQ_FMT_E2M1, M, H, K, gate_bf16, nullptr, gate_bias, nullptr};
     g.bf16 = true;
@@ -1098,7 +1130,7 @@ int mxq_gated_ffn(const void* x_bf16, int64_t M, int64_t K, const mxq_wdesc* gat
     RETURN_IF(check_gemm(workspace, workspace, up_fmt, M, K, gate->codes, gate->sf, H, gate->bias, workspace));
     RETURN_IF(check_gemm(workspace, workspace, up_fmt, M, K, up->codes, up->sf, H, up->bias, workspace));
     RETURN_IF(check_gemm(workspace, workspace, down_fmt, M, H, down->codes, down->sf, down->N, down->bias, y_bf16));
-    RETURN_IF(check_epilogue(e));
+    RETURN_IF(check_epilogue(e, M, down->N, y_bf16));
     if (e->act != MXQ_ACT_NONE)
         return fail(MXQ_ERR_INVALID_ARG, "gated ffn: the output's epilogue takes no activation (got %d)", e->act);
     const int64_t need = ffn_ws(M, K, H, up_fmt, down_fmt);

@@ -646,7 +646,7 @@ def gemm_residual(a_codes, a_sf, fmt, M: int, K: int, w: QWeight, act="none", re
                   rows_per_group=None, out=None, stream=None):
     """y = residual + gate * act(a . deq(w)^T + bias) [M, N] bf16, rounded once, on an
     already-quantized activation.  act "none", "gelu", "gelu_tanh" or "silu"; residual [M, N]
-    bf16 (it may be out); gate [groups, N] or [N], bf16 or float32, row m using group
+    bf16 (it may be out; otherwise out must not overlap it, nor the activation: refused); gate [groups, N] or [N], bf16 or float32, row m using group
     m // rows_per_group (default: one group)."""
     f = _fmt(fmt)
     dev = _operand(a_codes, a_sf, M, K, f)
@@ -662,7 +662,8 @@ def gemm_residual(a_codes, a_sf, fmt, M: int, K: int, w: QWeight, act="none", re
 def gemm_bf16_residual(a: torch.Tensor, b: torch.Tensor, bias: torch.Tensor | None = None, act="none", residual=None,
                        gate=None, rows_per_group=None, out=None, stream=None):
     """y = residual + gate * act(a . b^T + bias) in bf16 with fp32 accumulation, a [M, K] and
-    b [N, K] bf16; the other arguments as for gemm_residual."""
+    b [N, K] bf16; the other arguments as for gemm_residual.  out must not overlap a (refused),
+    also where a is the residual."""
     dev = _bf16_x(a, "a")
     M, K = a.shape
     N = b.shape[0]
@@ -710,7 +711,8 @@ def gemm_gated(a_codes, a_sf, fmt, M: int, K: int, gate: QWeight, up: QWeight, a
                codes=None, sf=None, stream=None):
     """h = act(a . deq(gate)^T + gate.bias) * (a . deq(up)^T + up.bias) [M, H] in one kernel,
     on an already-quantized activation.  Returns h in bf16, or, for out_fmt "e2m1" / "e4m3",
-    (codes, tiled scales): the bits that quantize_act writes for that h."""
+    (codes, tiled scales): the bits that quantize_act writes for that h.  No output may overlap
+    the activation (refused)."""
     f = _fmt(fmt)
     dev = _operand(a_codes, a_sf, M, K, f)
     dg, du = _qweight(gate, "gate", dev), _qweight(up, "up", dev)

@@ -449,13 +449,14 @@ int mxq_norm_residual(const mxq_norm_desc* d, void* z, int out_fmt, void* out, v
 typedef struct {
     int32_t act;            /* mxq_act                                                    */
     int32_t gate_dtype;     /* mxq_dtype of gate                                          */
-    const void* residual;   /* [M, N] bf16, or NULL (0); may be y                         */
+    const void* residual;   /* [M, N] bf16, or NULL (0); may be y, else apart from it     */
     const void* gate;       /* [groups, N], groups = ceil(M / rows_per_group), or NULL (1) */
     int64_t rows_per_group; /* > 0                                                        */
 } mxq_epilogue;
 
 /* mxq_gemm with activation, gate and residual in its epilogue.  Arguments and limits as for
- * mxq_gemm; residual and gate 16-byte aligned.  Few rows (64, or more of an output with few
+ * mxq_gemm; residual and gate 16-byte aligned.  y must not overlap the activation, nor a residual
+ * that is not y itself (refused).  Few rows (64, or more of an output with few
  * tiles) run on a kernel of their own that streams the weight (the tokens are the MMA's N
  * dimension, K is split over a cluster); its sums are formed in another order than the large
  * kernel's. */
@@ -463,7 +464,8 @@ int mxq_gemm_residual(const void* a_codes, const void* a_sf, int a_fmt, int64_t 
                       const void* w_sf, int64_t N, const void* bias_bf16, const mxq_epilogue* e, void* y_bf16,
                       void* stream);
 
-/* The same on bf16 operands, as mxq_gemm_bf16 takes them. */
+/* The same on bf16 operands, as mxq_gemm_bf16 takes them.  y must not overlap a (refused), also
+ * where a is the residual. */
 int mxq_gemm_bf16_residual(const void* a_bf16, int64_t M, int64_t K, const void* b_bf16, int64_t N,
                            const void* bias_bf16, const mxq_epilogue* e, void* y_bf16, void* stream);
 
@@ -481,7 +483,8 @@ int mxq_linear_residual(const void* x_bf16, int64_t M, int64_t K, const void* w_
  * with a the quantized activation (as for mxq_gemm; W4A8 needs K % 128 == 0 and 32-byte
  * aligned weights).  out_fmt MXQ_OUT_BF16: out receives h (H % 8 == 0), out_sf NULL.
  * MXQ_FMT_E2M1 / MXQ_FMT_E4M3: out and out_sf receive the codes and tiled scales that
- * mxq_quantize_act writes for h, padding included (H % 32 == 0, H <= 65536). */
+ * mxq_quantize_act writes for h, padding included (H % 32 == 0, H <= 65536).  Neither output may
+ * overlap the activation (refused). */
 int mxq_gemm_gated(const void* a_codes, const void* a_sf, int a_fmt, int64_t M, int64_t K, const mxq_wdesc* gate,
                    const mxq_wdesc* up, int act, int out_fmt, void* out, void* out_sf, void* stream);
 
