@@ -179,12 +179,6 @@ __device__ __forceinline__ float2 act_f32x2(float2 v)
     return v;
 }
 
-template <int kAct>
-__device__ __forceinline__ float act_f32(float v)
-{
-    return act_f32x2<kAct>(make_float2(v, v)).x;
-}
-
 // f(integral constant of the activation): the choice is taken once, outside f's loops.
 template <class F>
 __device__ __forceinline__ void with_act(int act, F&& f)

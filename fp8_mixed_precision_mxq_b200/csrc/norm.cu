@@ -635,8 +635,8 @@ cudaError_t launch_one(NormParams p, int warps, cudaStream_t stream)
 
 // Few rows: a CTA each, as many warps as a row has spans (two spans a warp from 16 on), for the
 // shortest chain of loads.  Many rows: CTAs of at most ten warps (more wait longer at each
-// barrier) with one chunk a thread of four rows or two of two rows (of one, for a bf16 stream with
-// bf16 out); longer rows take two or four chunks a thread of one row.
+// barrier) with one chunk a thread of four rows or, above ten spans, two of two rows (of one, for a
+// bf16 stream with bf16 out); rows of more than twenty spans take four chunks a thread of one row.
 template <bool kF32, bool kVF32, bool kQuant>
 cudaError_t launch_shape(const NormParams& p, cudaStream_t stream)
 {
@@ -656,9 +656,6 @@ cudaError_t launch_shape(const NormParams& p, cudaStream_t stream)
         return full ? launch_one<kF32, kVF32, kQuant, 1, 4, true, false>(p, warps, stream)
                     : launch_one<kF32, kVF32, kQuant, 1, 4, false, false>(p, warps, stream);
     constexpr int R = kF32 || kQuant ? 2 : 1;
-    if (spans > 20)
-        return full ? launch_one<kF32, kVF32, kQuant, 2, 1, true, false>(p, warps, stream)
-                    : launch_one<kF32, kVF32, kQuant, 2, 1, false, false>(p, warps, stream);
     return full ? launch_one<kF32, kVF32, kQuant, 2, R, true, false>(p, warps, stream)
                 : launch_one<kF32, kVF32, kQuant, 2, R, false, false>(p, warps, stream);
 }
