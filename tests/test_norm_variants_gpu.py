@@ -67,3 +67,20 @@ def test_results_repeat_bit_for_bit():
         first = ops.norm_residual(x, y, out_fmt="e4m3", **vecs)
         for _ in range(3):
             assert all(torch.equal(a, b) for a, b in zip(first, ops.norm_residual(x, y, out_fmt="e4m3", **vecs)))
+
+
+@pytest.mark.parametrize("rows", [2, 301])
+def test_codes_of_extreme_magnitudes(rows):
+    """Blocks of every size bf16 holds, subnormal and infinite ones too: the quantizer's bits."""
+    ops = _ops()
+    K = 32 * 288
+    x, _, _ = make(rows, K, rows)
+    weight = torch.exp2(torch.arange(288, device="cuda", dtype=torch.float64) - 150).clamp(max=2.0 ** 127).float()
+    weight = weight.repeat_interleave(32)
+    _, h = ops.norm_residual(x, norm="rms", weight=weight)
+    assert h.isinf().any() and (h == 0).any()
+    for fmt in ("e2m1", "e4m3"):
+        _, codes, sf = ops.norm_residual(x, norm="rms", weight=weight, out_fmt=fmt)
+        want_c, want_s = ops.quantize_act(h, fmt)
+        assert torch.equal(codes, want_c) and torch.equal(sf, want_s), fmt
+    assert ops.poll_status() == 0
