@@ -37,10 +37,10 @@
 // registers (no shared-memory staging, no TMA store): the residual one, y = bf16(residual +
 // gate * act(acc + bias)), and the gated one, whose tile is 128 columns of each of a gated
 // feed-forward network's two projections (the leader loads one weight's rows, the other CTA the
-// other's) and which writes act(g + bg) * (u + bu), as bf16 or MX-quantized.  Measured beside the
-// plain GEMM on 32760 rows (W4A4): 5120 x 5120 with residual and gate 482 us (431), erf GELU
-// 499; both 13824-column projections of 5120 with SiLU and E2M1 out 2227 us (2065 for a plain
-// GEMM of 27648 columns).  What bounds them is what bounds the plain GEMM: operand traffic from
+// other's) and which writes act(g + bg) * (u + bu), as bf16 or MX-quantized.  Measured in turn with
+// the plain GEMM, back to back, on 32760 rows (W4A4): 5120 x 5120 with residual and gate 486 us
+// (plain 429), with erf GELU too 542; both 13824-column projections of 5120 with SiLU and E2M1 out
+// 2293 us (2138 for a plain GEMM of 27648 columns).  What bounds them is what bounds the plain GEMM: operand traffic from
 // L2 and, in long runs, the power cap; the tensor pipe is active 48-49 % of the cycles.
 // L2 policies: the weight is loaded evict-last (it is reused by every m-block and fits
 // in L2), the output is stored evict-first.
@@ -147,7 +147,7 @@ template <int kOut>  // the next layer's MX operand is written
 constexpr bool kOutQuant = (kOut >= kOutGeluE2M1 && kOut <= kOutQE4M3) || kOut >= kOutGatedE2M1;
 // The residual and gated epilogues store from their registers, 32 bytes a lane: a whole sector,
 // which TMA stores of 64-byte rows behind the mainloop's loads, and 16-byte stores, do not
-// match (32760 x 5120 x 5120 W4A4 with residual and gate: 448 us, against 586 and 534).
+// match (32760 x 5120 x 5120 W4A4 with residual and gate, single calls: 448 us, against 586 and 534).
 template <int kOut>
 constexpr bool kOutDirect = kOut >= kOutRes;
 template <int kOut>  // GELU from the table

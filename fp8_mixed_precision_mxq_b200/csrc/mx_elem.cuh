@@ -130,7 +130,8 @@ __device__ __forceinline__ uint32_t gelu_bf16_bits(uint32_t b, const uint16_t* l
 // Applied to the binary32 sum, so that the result is rounded to bf16 once; two values at a time
 // on packed fp32 pairs.  The two sigmoid forms v / (1 + exp(-t)) keep their relative accuracy
 // where v is far negative (1 + tanh would cancel there), and so does the erf form, which takes
-// the tail's own function.
+// the tail's own function; where 1 + exp passes 2^126 (SiLU below v = -87.3) the quotient is 0, for
+// a value below 2^-119.
 __device__ __forceinline__ float ex2_approx(float x)
 {
     float y;

@@ -30,11 +30,13 @@ namespace {
 
 constexpr int kMaxThreads = 1024, kMaxWarps = kMaxThreads / 32;
 
-// Registers a thread may take: what lets the most rows be under way on an SM without spilling the
-// row itself.  Measured at 32760 x 5120 (gate, scale and shift in fp32): one row of two chunks a
-// thread at 48 registers 240 us (bf16 out), at 56 269, at 40 273; two rows at 64 registers 284,
-// but with E4M3 out 559 us (75600 rows) against 591; an fp32 stream two rows at 80 registers 317
-// us, one row at 64 374.
+// Registers a thread may take, so that many rows are under way on an SM.  Measured at 5120 channels
+// only (32760 rows; gate, scale and shift in fp32): one row of two chunks a thread at 48 registers
+// 240 us (bf16 out), at 56 269, at 40 273; two rows at 64 registers 284, but with E4M3 out 559 us
+// (75600 rows) against 591; an fp32 stream two rows at 80 registers 317 us, one row at 64 374.
+// The budgets do not hold everything: with one or two rows of two chunks only the kernels of a
+// bf16 stream with MX out spill (92-136 bytes a thread), but with four rows of one chunk a bf16
+// stream spills 80-144 bytes, and with four chunks a thread every kernel 92-364.
 constexpr int norm_regs(bool f32, int c, int r, bool early)
 {
     return early ? 128 : c * r < 4 ? (f32 ? 64 : 48) : f32 && c < 4 ? 80 : 64;
@@ -459,11 +461,13 @@ __device__ __forceinline__ void emit(const NormParams& p, int64_t row, size_t ba
     }
 }
 
-// A CTA takes R rows of one group.  kF32: the residual stream x, z is fp32 (else bf16); kVF32: so
-// are the channel vectors.  kQuant: h leaves as MX codes (else bf16).  C: chunks of 8 channels
-// per thread and row; chunk j of warp w is its lanes' part of span j * warps + w, whose MX blocks
-// lie in eight lanes each.  kFull: a row has exactly C * warps spans (else some channels are past
-// its end).  kEarly: the last step's vectors are fetched with the rows.
+// A CTA takes up to R rows of one group (of groups shorter than R rows, fewer: the rest of its work
+// is thrown away; vectors of one row each, 32760 x 2048, 375 us against 107 with one group).  kF32:
+// the residual stream x, z is fp32 (else bf16); kVF32: so are the channel vectors.  kQuant: h
+// leaves as MX codes (else bf16).  C: chunks of 8 channels per thread and row; chunk j of warp w is
+// its lanes' part of span j * warps + w, whose MX blocks lie in eight lanes each.  kFull: a row has
+// exactly C * warps spans (else some channels are past its end).  kEarly: the last step's vectors
+// are fetched with the rows.
 // What keeps the kernel from the memory's rate is its own work, so: R rows share each vector's
 // loads and each barrier; arithmetic runs on packed fp32 pairs; a bf16 z is held packed between
 // the passes over it, which leaves registers for more rows on an SM; and each optional vector is
@@ -471,8 +475,9 @@ __device__ __forceinline__ void emit(const NormParams& p, int64_t row, size_t ba
 // became predicates, and a launch issued every option's instructions: 41 an element).  Many small
 // CTAs hide each other's barriers: persistent CTAs, with the next row prefetched into shared
 // memory, into L2 or into registers, all measured 20 to 60 % slower.
-// Measured (share of the copy rate): 32760 x 5120 with gate, scale, shift in fp32, bf16 out 241 us
-// (86 %), of an fp32 stream 318 us (98 %); 75600 x 5120 with E4M3 out 555 us (76 %).
+// Measured (share of the copy rate): 32760 x 5120 with gate, scale, shift in fp32, bf16 out 229-248 us
+// (84-91 %), of an fp32 stream 309 us; 75600 x 5120 with E4M3 out 540-610 us (78-69 %; the slower end
+// with the GPU idle between calls or after long runs).
 template <bool kF32, bool kVF32, bool kQuant, int C, int R, bool kFull, bool kEarly>
 __global__ void __maxnreg__(norm_regs(kF32, C, R, kEarly)) norm_residual_kernel(const NormParams p)
 {
@@ -633,10 +638,11 @@ cudaError_t launch_one(NormParams p, int warps, cudaStream_t stream)
     return cudaGetLastError();
 }
 
-// Few rows: a CTA each, as many warps as a row has spans (two spans a warp from 16 on), for the
-// shortest chain of loads.  Many rows: CTAs of at most ten warps (more wait longer at each
-// barrier) with one chunk a thread of four rows or, above ten spans, two of two rows (of one, for a
-// bf16 stream with bf16 out); rows of more than twenty spans take four chunks a thread of one row.
+// Few rows (two a multiprocessor of the B200's 148): a CTA each, as many warps as a row has spans
+// (two spans a warp from 17 on), for the shortest chain of loads.  Many rows: CTAs of at most ten
+// warps (more wait longer at each barrier) with one chunk a thread of four rows or, above ten
+// spans, two of two rows (of one, for a bf16 stream with bf16 out); rows of more than twenty spans
+// take four chunks a thread of one row, and up to 32 warps.
 template <bool kF32, bool kVF32, bool kQuant>
 cudaError_t launch_shape(const NormParams& p, cudaStream_t stream)
 {
