@@ -137,3 +137,36 @@ def test_split_on_another_stream():
     got = ops.svd_split(w, 8, stream=side)
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_captured_on_a_forked_stream():
+    """Calls given a stream that joins a capture: their memory is the graph's, and replays repeat."""
+    ops = _ops()
+    g = torch.Generator(device="cuda").manual_seed(4)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda").bfloat16()  # noqa: E731
+    x, y = rnd(M, K), rnd(M, K)
+    wg, wu, wd = ops.quantize_weight(rnd(H, K)), ops.quantize_weight(rnd(H, K)), ops.quantize_weight(rnd(K, H))
+    x1, y1 = rnd(M, K), rnd(M, K)
+
+    def block(a, b, st):
+        z, h = ops.norm_residual(a, b, stream=st)
+        return ops.gated_ffn(h, wg, wu, wd, residual=z, stream=st)
+
+    want = [block(x, y, None), block(x1, y1, None)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph, out = torch.cuda.CUDAGraph(), torch.empty_like(x)
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        got = block(x, y, side)
+        torch.cuda.current_stream().wait_stream(side)
+        out.copy_(got)
+        del got
+    for a, b, w in ((x1, y1, want[1]), (x.clone(), y.clone(), want[0]), (x1, y1, want[1])):
+        x.copy_(a)
+        y.copy_(b)
+        graph.replay()
+        junk = [torch.full((M, K), 9.0, device="cuda").bfloat16() for _ in range(4)]
+        assert torch.equal(out, w)
+        del junk
+    assert ops.poll_status() == 0
